@@ -9,6 +9,7 @@
 #include <mutex>
 
 #include "kda.h"
+#include "kda_check.cuh"
 #include "kda_internal.cuh"
 #include "kda_tmap.cuh"
 
@@ -67,29 +68,7 @@ int debug_stall() { return g_stall.load(std::memory_order_relaxed); }
 
 namespace {
 
-bool supported_d(int d) { return d == 16 || d == 32 || d == 64 || d == 128; }
-
-bool aligned16(const void *p) { return ((uintptr_t)p & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-};
-
-Range range_of(const void *p, size_t bytes) {
-  return Range{(uintptr_t)p, (uintptr_t)p + bytes};
-}
-
-bool overlap(Range a, Range b) { return a.lo < b.hi && b.lo < a.hi && a.lo != a.hi && b.lo != b.hi; }
-
-// Device must be a Blackwell datacenter part (compute capability 10.x): the
-// library is compiled for sm_100a only.
-kda_status_t check_device() {
-  int dev = 0, major = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return KDA_ERR_CUDA;
-  if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess)
-    return KDA_ERR_CUDA;
-  return major == 10 ? KDA_OK : KDA_ERR_UNSUPPORTED;
-}
+using namespace kda::check;
 
 kda_status_t plan_prefill(int B, int H, int T, int dk, int dv, kda_dtype_t dtype, int chunk_size,
                           kda_plan_t *plan) {

@@ -1,0 +1,127 @@
+// Block tables and token slots from request lengths (include/kda.h,
+// kda_block_map): sequence offsets, the blocks that the new tokens need, and
+// the pool slot of every new token.
+//
+// The work is two prefix sums over the requests (tokens, and new blocks) and
+// one lookup a token, so a launch's latency and the 8 bytes a token bound it.
+// One launch does all: every block forms both prefix sums itself (R lengths
+// and contexts from L2, two integers a request in shared memory) instead of
+// waiting for another block, takes its own tile of rows, and finds a row's
+// request by bisection in shared memory.  A token in a new block takes the
+// block from free_pages, not from the table, so no block waits for the
+// table's update, which is spread over the blocks request by request.
+#include "kda_serve.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowsPerBlock = 1024;
+constexpr int kMaxR = 16384;
+
+__device__ __forceinline__ int64_t blocks_of(int64_t tokens, int page) { return (tokens + page - 1) / page; }
+
+__device__ __forceinline__ int saturate(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int)v; }
+
+__global__ void __launch_bounds__(kThreads) block_map_kernel(MapArgs a) {
+  extern __shared__ int sh[];  // [R + 1] row offsets, [R + 1] new-block offsets
+  int *s_cu = sh, *s_new = sh + a.R + 1;
+  __shared__ int64_t w_tok[kThreads / 32], w_blk[kThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+  // exclusive prefix sums, kThreads requests at a time (64 bits: garbage lengths must not wrap)
+  int64_t tok0 = 0, blk0 = 0;
+  for (int r0 = 0; r0 < a.R; r0 += kThreads) {
+    const int r = r0 + tid;
+    int64_t n = 0, b = 0;
+    if (r < a.R) {
+      n = max(a.len[r], 0);
+      const int64_t c = a.ctx ? max(a.ctx[r], 0) : 0;
+      b = blocks_of(c + n, a.page) - blocks_of(c, a.page);
+    }
+    int64_t in = n, ib = b;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(~0u, in, o), y = __shfl_up_sync(~0u, ib, o);
+      if (lane >= o) { in += x; ib += y; }
+    }
+    if (lane == 31) { w_tok[warp] = in; w_blk[warp] = ib; }
+    __syncthreads();
+    int64_t bt = tok0, bb = blk0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+      if (w < warp) { bt += w_tok[w]; bb += w_blk[w]; }
+      tok0 += w_tok[w];
+      blk0 += w_blk[w];
+    }
+    if (r < a.R) {
+      s_cu[r] = saturate(bt + in - n);
+      s_new[r] = saturate(bb + ib - b);
+    }
+    __syncthreads();
+  }
+  if (tid == 0) {
+    s_cu[a.R] = saturate(tok0);
+    s_new[a.R] = saturate(blk0);
+  }
+  __syncthreads();
+
+  if (blockIdx.x == 0) {
+    for (int r = tid; r <= a.R; r += kThreads) a.cu[r] = s_cu[r];
+    if (tid == 0) a.used[0] = s_new[a.R];
+  }
+  // new table entries: one warp a request
+  for (int r = blockIdx.x * (kThreads / 32) + warp; r < a.R; r += gridDim.x * (kThreads / 32)) {
+    const int n = s_new[r + 1] - s_new[r];
+    if (n <= 0) continue;
+    const int64_t old = blocks_of(a.ctx ? max(a.ctx[r], 0) : 0, a.page);
+    for (int64_t j = lane; j < n && j < a.table_stride - old; j += 32) {
+      const int64_t f = s_new[r] + j;
+      a.table[(int64_t)r * a.table_stride + old + j] = f < a.n_free ? a.free_pages[f] : -1;
+    }
+  }
+  const int row0 = blockIdx.x * kRowsPerBlock;
+  for (int i = tid; i < kRowsPerBlock; i += kThreads) {
+    const int row = row0 + i;
+    if (row >= a.rows) break;
+    int64_t slot = -1;
+    if (row < s_cu[a.R]) {
+      int lo = 0, hi = a.R;  // s_cu[lo] <= row < s_cu[hi]
+      while (hi - lo > 1) {
+        const int m = (lo + hi) >> 1;
+        if (s_cu[m] <= row) lo = m; else hi = m;
+      }
+      const int64_t c = a.ctx ? max(a.ctx[lo], 0) : 0;
+      const int64_t pos = c + row - s_cu[lo];
+      const int64_t j = pos / a.page;
+      const int64_t old = blocks_of(c, a.page);
+      if (j < a.table_stride) {
+        int64_t page = -1;
+        if (j < old) {
+          page = a.table[(int64_t)lo * a.table_stride + j];
+        } else {
+          const int64_t f = s_new[lo] + (j - old);
+          if (f < a.n_free) page = a.free_pages[f];
+        }
+        if (page >= 0) slot = page * a.page + pos % a.page;
+      }
+    }
+    a.token_slots[row] = slot;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_block_map(const MapArgs &a, cudaStream_t st) {
+  const size_t smem = 2 * sizeof(int) * ((size_t)a.R + 1);
+  static_assert(2 * sizeof(int) * (kMaxR + 1) <= 200 * 1024, "prefix sums in shared memory");
+  if (smem > 48 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(block_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int grid = max(1, (int)(((int64_t)a.rows + kRowsPerBlock - 1) / kRowsPerBlock));
+  block_map_kernel<<<grid, kThreads, smem, st>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace kda

@@ -1,0 +1,205 @@
+// Selective state space scan of packed prompts (include/kda.h, kda_ssm_scan):
+// the CUDA-core kernel (fp32 and any size), and the segment bookkeeping that
+// every scan kernel shares.
+//
+//     S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T,    y_t = S_t^T C_t + D x_t.
+//
+// Where the sequences and heads alone do not fill the machine, sequences are
+// cut into segments.  The recurrence is linear in the entering state and its
+// transition is one number, so a segment maps S to S~ + a S, a = exp(A sum d):
+// a first pass computes (S~, a) of every segment but the last of its sequence
+// from a zero state, a second walks down the segments and leaves each one's
+// entering state, and the last pass runs all segments from those.  No block
+// waits for another one.
+//
+// The CUDA-core kernel: one CTA a (segment, head).  Four neighbouring lanes
+// share a state column, each holding a quarter of its N rows in registers, so
+// the token loop has no barrier: a token costs 3 N / 4 operations a thread and
+// two shuffles.  Tokens are staged in shared memory TB at a time.  Its chain of
+// dependent tokens bounds it, not bytes.
+#include "kda_ssm_seg.cuh"
+
+namespace kda {
+namespace {
+
+constexpr int TB = 16;  // tokens staged at a time
+
+template <int N, int P, typename T, bool kOut>
+__global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, float *ws, float *decays) {
+  constexpr int NT = 4 * P, J = N / 16;  // a thread holds J blocks of 4 rows
+  __shared__ __align__(16) float sB[TB][N];
+  __shared__ __align__(16) float sC[kOut ? TB : 1][N];
+  __shared__ float sx[TB][P], sy[kOut ? TB : 1][P], sd[TB], sa[TB];
+  const int tid = threadIdx.x, p = tid >> 2, quarter = tid & 3;
+  const int h = blockIdx.x % a.H;
+  const bool tell = h == 0 && tid == 0;
+  Item it;
+  if (!item_of(a.q, blockIdx.x / a.H, seg, tell, it)) return;
+  if (!kOut && it.index == it.count - 1) return;  // nothing follows it
+  const int g = h / (a.H / a.G);
+  float S[J][4];  // rows 16 j + 4 quarter + i
+  const int64_t at = (it.item * a.H + h) * (N * P);
+  const float *from = nullptr;
+  if (kOut) {
+    if (seg != 0) from = ws + at;
+    else if (a.state && it.s.ctx > 0) from = a.state + ((int64_t)it.s.slot * a.H + h) * (N * P);
+  }
+#pragma unroll
+  for (int j = 0; j < J; ++j)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) S[j][i] = from ? from[(16 * j + 4 * quarter + i) * P + p] : 0.f;
+  auto save = [&](float *to) {
+#pragma unroll
+    for (int j = 0; j < J; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) to[(16 * j + 4 * quarter + i) * P + p] = S[j][i];
+  };
+  const float A = a.A[h], skip = a.D ? a.D[h] : 0.f;
+  float total = 0.f;  // sum of d (thread 0)
+
+  for (int t0 = it.begin; t0 < it.end; t0 += TB) {
+    const int nt = min(TB, it.end - t0);
+    const int64_t row0 = (int64_t)it.s.start + t0;
+    __syncthreads();
+    for (int e = tid; e < nt * N; e += NT) {
+      const int t = e / N, n = e % N;
+      sB[t][n] = as_float(((const T *)a.B)[(row0 + t) * a.b_stride + g * N + n]);
+      if (kOut) sC[t][n] = as_float(((const T *)a.C)[(row0 + t) * a.c_stride + g * N + n]);
+    }
+    for (int e = tid; e < nt * P; e += NT) {
+      const int t = e / P, c = e % P;
+      sx[t][c] = as_float(((const T *)a.x)[(row0 + t) * a.x_stride + h * P + c]);
+    }
+    if (tid < nt) {
+      const float d = time_step<T>(a, row0 + tid, h);
+      sd[tid] = d;
+      sa[tid] = expf(d * A);
+    }
+    __syncthreads();
+    if (!kOut && tid == 0)
+      for (int t = 0; t < nt; ++t) total += sd[t];
+    for (int t = 0; t < nt; ++t) {
+      const float keep = sa[t], xv = sx[t][p], dx = sd[t] * xv;
+      float y = 0.f;
+#pragma unroll
+      for (int j = 0; j < J; ++j) {
+        const float4 b = *reinterpret_cast<const float4 *>(&sB[t][16 * j + 4 * quarter]);
+        S[j][0] = fmaf(b.x, dx, keep * S[j][0]);
+        S[j][1] = fmaf(b.y, dx, keep * S[j][1]);
+        S[j][2] = fmaf(b.z, dx, keep * S[j][2]);
+        S[j][3] = fmaf(b.w, dx, keep * S[j][3]);
+        if (kOut) {
+          const float4 c = *reinterpret_cast<const float4 *>(&sC[t][16 * j + 4 * quarter]);
+          y = fmaf(c.x, S[j][0], y);
+          y = fmaf(c.y, S[j][1], y);
+          y = fmaf(c.z, S[j][2], y);
+          y = fmaf(c.w, S[j][3], y);
+        }
+      }
+      if (kOut) {
+        y += __shfl_xor_sync(~0u, y, 1);
+        y += __shfl_xor_sync(~0u, y, 2);
+        if (quarter == 0) sy[t][p] = fmaf(skip, xv, y);
+        if (a.page)
+          if (float *to = snapshot(a, it.r, h, (int64_t)it.s.ctx + t0 + t + 1, tell)) save(to);
+      }
+    }
+    if (kOut) {
+      __syncthreads();
+      for (int e = tid; e < nt * P; e += NT) {
+        const int t = e / P, c = e % P;
+        ((T *)a.y)[(row0 + t) * a.y_stride + h * P + c] = as_type<T>(sy[t][c]);
+      }
+    }
+  }
+  if (!kOut) {
+    save(ws + at);
+    if (tid == 0) decays[it.item * a.H + h] = expf(A * total);
+  } else if (a.state && it.index == it.count - 1) {
+    save(a.state + ((int64_t)it.s.slot * a.H + h) * (N * P));
+  }
+}
+
+// Entering states of every segment of a sequence, in place of what the segments
+// add to a zero state: S(0) from the pool, S(i + 1) = a_i S(i) + S~_i.
+constexpr int kJoinThreads = 128;
+__global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a, int seg, float4 *ws,
+                                                                      const float *decays) {
+  const int r = blockIdx.x / a.H, h = blockIdx.x % a.H;
+  const int n4 = a.N * a.P / 4, e = blockIdx.y * kJoinThreads + threadIdx.x;
+  const Seq s = seq_of(a.q, r, false);
+  const int len = s.end - s.start;
+  if (e >= n4 || !s.ok || len == 0) return;
+  const int64_t base = seg_base(a.q, r, seg);
+  const int count = (int)(((int64_t)(s.ctx % kAlign) + len + seg - 1) / seg);
+  float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (a.state && s.ctx > 0)
+    S = reinterpret_cast<const float4 *>(a.state)[((int64_t)s.slot * a.H + h) * n4 + e];
+  for (int i = 0; i < count; ++i) {
+    float4 *w = ws + ((base + i) * a.H + h) * n4 + e;
+    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
+    float keep = 0.f;
+    if (i + 1 < count) {
+      add = *w;
+      keep = decays[(base + i) * a.H + h];
+    }
+    *w = S;
+    S.x = fmaf(keep, S.x, add.x);
+    S.y = fmaf(keep, S.y, add.y);
+    S.z = fmaf(keep, S.z, add.z);
+    S.w = fmaf(keep, S.w, add.w);
+  }
+}
+
+// Segment length of the CUDA-core kernel: none while the sequences' heads give
+// every SM a block (or prompts are short), else as many as do.
+int simt_segment(int R, int rows, int H) {
+  const int64_t chains = (int64_t)R * H;
+  if (chains >= 148 || rows < 2 * kAlign) return 0;
+  const int64_t want = (148 + H - 1) / H;  // segments in all
+  const int64_t seg = ((rows + want - 1) / want + kAlign - 1) / kAlign * kAlign;
+  return (int)seg;
+}
+
+template <int N, int P, typename T>
+cudaError_t launch_t(const SsmArgs &a, int seg, cudaStream_t st) {
+  const int64_t items = scan_items(a.q.R, a.q.rows, seg);
+  float *ws = seg ? seg_states(a) : nullptr, *dec = seg ? seg_decays(a, items) : nullptr;
+  const unsigned grid = (unsigned)(items * a.H);
+  if (seg) {
+    ssm_scan_kernel<N, P, T, false><<<grid, 4 * P, 0, st>>>(a, seg, ws, dec);
+    cudaError_t e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_segment_states(a, seg, st);
+    if (e != cudaSuccess) return e;
+  }
+  ssm_scan_kernel<N, P, T, true><<<grid, 4 * P, 0, st>>>(a, seg, ws, dec);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_segment_states(const SsmArgs &a, int seg, cudaStream_t st) {
+  const dim3 grid((unsigned)((int64_t)a.q.R * a.H), (a.N * a.P / 4 + kJoinThreads - 1) / kJoinThreads);
+  segment_states_kernel<<<grid, kJoinThreads, 0, st>>>(a, seg, (float4 *)seg_states(a),
+                                                       seg_decays(a, scan_items(a.q.R, a.q.rows, seg)));
+  return cudaGetLastError();
+}
+
+size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16) {
+  const int seg = simt_segment(R, rows, H);
+  return seg ? seg_workspace(scan_items(R, rows, seg), H, N, P) : 0;
+}
+
+cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st) {
+  const int seg = simt_segment(a.q.R, a.q.rows, a.H);
+#define KDA_SSM_CASE(NN, PP)    \
+  if (a.N == NN && a.P == PP)   \
+    return a.bf16 ? launch_t<NN, PP, __nv_bfloat16>(a, seg, st) : launch_t<NN, PP, float>(a, seg, st);
+#define KDA_SSM_ROW(NN) KDA_SSM_CASE(NN, 16) KDA_SSM_CASE(NN, 32) KDA_SSM_CASE(NN, 64) KDA_SSM_CASE(NN, 128)
+  KDA_SSM_ROW(16) KDA_SSM_ROW(32) KDA_SSM_ROW(64) KDA_SSM_ROW(128)
+#undef KDA_SSM_ROW
+#undef KDA_SSM_CASE
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace kda

@@ -18,6 +18,7 @@ SO = os.path.join(PKG, "libkda.so")
 KDA_OK = 0
 KDA_DTYPE_F32 = 0
 KDA_DTYPE_BF16 = 1
+KDA_CONV_SILU, KDA_CONV_L2NORM, KDA_CONV_HEAD_MAJOR = 1, 2, 4
 KDA_PATH_AUTO, KDA_PATH_SIMT16, KDA_PATH_TC32 = 0, 1, 2
 STATUS_NAMES = ["KDA_OK", "KDA_ERR_INVALID_ARG", "KDA_ERR_SHAPE", "KDA_ERR_DTYPE", "KDA_ERR_ALIGNMENT",
                 "KDA_ERR_ALIAS", "KDA_ERR_WORKSPACE", "KDA_ERR_CUDA", "KDA_ERR_TIMEOUT",
@@ -26,7 +27,8 @@ EXPORTED = ["kda_chunk_fwd_plan", "kda_chunk_fwd_workspace_size", "kda_chunk_fwd
             "kda_status_string", "kda_get_device_status", "kda_version", "kda_chunk_fwd_noalloc",
             "kda_noalloc_scratch_bytes", "kda_chunk_fwd_ckpt", "kda_chunk_fwd_gated", "kda_output_gate",
             "kda_kcp_compose", "kda_spec_replay_verify", "kda_debug_set_wait_limit", "kda_debug_inject_stall",
-            "kda_chunk_fwd_outgate", "kda_chunk_transition", "kda_spec_replay_verify_fused"]
+            "kda_chunk_fwd_outgate", "kda_chunk_transition", "kda_spec_replay_verify_fused", "kda_block_map",
+            "kda_short_conv", "kda_short_conv_step", "kda_ssm_scan", "kda_ssm_scan_workspace_size", "kda_ssm_step"]
 
 
 class KdaError(RuntimeError):
@@ -93,6 +95,20 @@ def load_library():
             lib.kda_chunk_fwd_noalloc.restype = i
             lib.kda_noalloc_scratch_bytes.argtypes = []
             lib.kda_noalloc_scratch_bytes.restype = sz
+            ll = ctypes.c_longlong
+            lib.kda_block_map.argtypes = [vp, vp, vp, i, vp, i, i, vp, vp, vp, i, i, vp]
+            lib.kda_block_map.restype = i
+            lib.kda_short_conv.argtypes = [vp, ll, vp, vp, vp, i, vp, vp, vp, vp, ll] + [i] * 7 + [f, vp]
+            lib.kda_short_conv.restype = i
+            lib.kda_short_conv_step.argtypes = [vp, ll, vp, vp, vp, i, vp, vp, ll] + [i] * 6 + [f, vp]
+            lib.kda_short_conv_step.restype = i
+            lib.kda_ssm_scan.argtypes = ([vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, i, vp, i, vp, vp, vp, vp, i, vp, i, i,
+                                          vp, ll] + [i] * 7 + [vp, sz, vp])
+            lib.kda_ssm_scan.restype = i
+            lib.kda_ssm_scan_workspace_size.argtypes = [i] * 7
+            lib.kda_ssm_scan_workspace_size.restype = sz
+            lib.kda_ssm_step.argtypes = [vp, ll, vp, ll, vp, vp, ll, vp, ll, vp, vp, i, vp, i, vp, vp, ll] + [i] * 6 + [vp]
+            lib.kda_ssm_step.restype = i
             _lib = lib
     return _lib
 
@@ -193,6 +209,48 @@ def kda_noalloc_scratch_bytes() -> int:
 
 def kda_recurrent_step(q, k, v, g, beta, S, o, B, H, dk, dv, dtype, scale, stream) -> int:
     return load_library().kda_recurrent_step(q, k, v, g, beta, S, o, B, H, dk, dv, dtype, scale, stream)
+
+
+def kda_block_map(length, ctx, free_pages, n_free, block_table, table_stride, page_size, cu, token_slots, pages_used, R,
+                  rows, stream) -> int:
+    """Block tables and token slots from request lengths.  Returns the raw kda_status_t."""
+    return load_library().kda_block_map(length, ctx, free_pages, n_free, block_table, table_stride, page_size, cu,
+                                        token_slots, pages_used, R, rows, stream)
+
+
+def kda_short_conv(x, x_stride, w, bias, state, n_slots, slots, ctx, cu, y, y_stride, R, rows, C, K, head_dim, dtype,
+                   flags, eps, stream) -> int:
+    """Short causal convolution of packed prompts.  Returns the raw kda_status_t."""
+    return load_library().kda_short_conv(x, x_stride, w, bias, state, n_slots, slots, ctx, cu, y, y_stride, R, rows, C, K,
+                                         head_dim, dtype, flags, eps, stream)
+
+
+def kda_short_conv_step(x, x_stride, w, bias, state, n_slots, slots, y, y_stride, R, C, K, head_dim, dtype, flags, eps,
+                        stream) -> int:
+    """Short causal convolution of single tokens.  Returns the raw kda_status_t."""
+    return load_library().kda_short_conv_step(x, x_stride, w, bias, state, n_slots, slots, y, y_stride, R, C, K, head_dim,
+                                              dtype, flags, eps, stream)
+
+
+def kda_ssm_scan(x, x_stride, dt, dt_stride, A, B, b_stride, C, c_stride, D, dt_bias, softplus, state, n_slots, slots,
+                 ctx, cu, block_table, table_stride, pages, n_pages, page_size, y, y_stride, R, rows, H, G, N, P, dtype,
+                 workspace, workspace_bytes, stream) -> int:
+    """Selective state space scan of packed prompts.  Returns the raw kda_status_t."""
+    return load_library().kda_ssm_scan(x, x_stride, dt, dt_stride, A, B, b_stride, C, c_stride, D, dt_bias, softplus,
+                                       state, n_slots, slots, ctx, cu, block_table, table_stride, pages, n_pages,
+                                       page_size, y, y_stride, R, rows, H, G, N, P, dtype, workspace, workspace_bytes,
+                                       stream)
+
+
+def kda_ssm_scan_workspace_size(R, rows, H, G, N, P, dtype) -> int:
+    return load_library().kda_ssm_scan_workspace_size(R, rows, H, G, N, P, dtype)
+
+
+def kda_ssm_step(x, x_stride, dt, dt_stride, A, B, b_stride, C, c_stride, D, dt_bias, softplus, state, n_slots, slots, y,
+                 y_stride, R, H, G, N, P, dtype, stream) -> int:
+    """Selective state space step of single tokens.  Returns the raw kda_status_t."""
+    return load_library().kda_ssm_step(x, x_stride, dt, dt_stride, A, B, b_stride, C, c_stride, D, dt_bias, softplus,
+                                       state, n_slots, slots, y, y_stride, R, H, G, N, P, dtype, stream)
 
 
 def kda_get_device_status(stream=None) -> int:
@@ -405,4 +463,284 @@ def spec_replay_verify_fused(q, k, v, z, A_log, beta, S, gate, rms_weight, n_rep
                                       W, dk, dv, _dtype_code(q), float(scale), _stream(stream))
     if st != KDA_OK:
         raise KdaError(st, "kda_spec_replay_verify_fused")
+    return y
+
+
+# ---- packed requests (kda_block_map, kda_short_conv*, kda_ssm_*) ---------------
+#
+# Token-major arguments may be row-strided views (the columns of a wider
+# projection, or of the convolution's output): only the elements of a row have
+# to be dense.  Integer arguments (cu, ctx, slots, lengths, tables) are int32
+# tensors on the same device and are not read on the host.
+
+def _on(device, *tensors):
+    for t in tensors:
+        if t is not None and t.device != device:
+            raise ValueError("all tensors of a call must be on one CUDA device (got %s and %s)" % (device, t.device))
+
+
+def _typed(dtype, **tensors):
+    import torch
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), t.dtype))
+
+
+def _shaped(name, t, shape):
+    if t is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+
+
+def _rows(name, t, lead, cuda=True):
+    """Row stride of token-major `t`: `lead` leading dimensions of rows over dense rows of elements."""
+    if cuda and not t.is_cuda:
+        raise ValueError("libkda takes CUDA tensors")
+    shape, stride = t.shape, t.stride()
+    want = 1
+    for i in range(t.dim() - 1, lead - 1, -1):
+        if shape[i] != 1 and stride[i] != want:
+            raise ValueError("%s: the elements of a row must be dense" % name)
+        want *= shape[i]
+    if lead == 2 and shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * stride[1]:
+        raise ValueError("%s: rows must have one stride" % name)
+    rows = shape[0] if lead == 1 else shape[0] * shape[1]
+    if rows <= 1:
+        return want
+    return stride[lead - 1] if shape[lead - 1] > 1 else stride[0]
+
+
+class _Call:
+    """The device's stream for a call, with that device current."""
+
+    def __init__(self, device, stream):
+        import torch
+        self.other = None if device.index is None or device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        self.stream, self.device = stream, device
+
+    def __enter__(self):
+        import torch
+        if self.other is not None:
+            self.other.__enter__()
+        if self.stream is None:
+            return torch.cuda.current_stream(self.device).cuda_stream
+        return getattr(self.stream, "cuda_stream", self.stream)
+
+    def __exit__(self, *exc):
+        if self.other is not None:
+            self.other.__exit__(*exc)
+
+
+def _check(code, what):
+    if code != KDA_OK:
+        raise KdaError(code, what)
+
+
+def _requests(x, lead, state, slots, ctx, cu):
+    """(R, rows) of a packed call, after the checks of its integer arguments."""
+    import torch
+    _typed(torch.int32, slots=slots, ctx=ctx, cu=cu)
+    if lead == 2:
+        if cu is not None:
+            raise ValueError("cu goes with [rows, ...] tensors")
+        R, rows = x.shape[0], x.shape[0] * x.shape[1]
+    else:
+        rows = x.shape[0]
+        R = 1 if cu is None else cu.numel() - 1
+        if R < 0:
+            raise ValueError("cu must hold R + 1 offsets")
+    _shaped("slots", slots, (R,))
+    _shaped("ctx", ctx, (R,))
+    return R, rows
+
+
+def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, token_slots=None, pages_used=None,
+              stream=None):
+    """Sequence offsets, block table and token slots from request lengths, on the
+    device (kda_block_map).  lens, ctx (or None): [R] int32; free_pages: [n]
+    int32; block_table: [R, blocks] int32, updated in place; rows: the most new
+    tokens that the call may hold.  Returns (cu [R + 1] int32, token_slots [rows]
+    int64, pages_used [1] int32)."""
+    import torch
+    _typed(torch.int32, lens=lens, ctx=ctx, free_pages=free_pages, block_table=block_table, cu=cu, pages_used=pages_used)
+    _typed(torch.int64, token_slots=token_slots)
+    dev, R = lens.device, lens.numel()
+    _on(dev, ctx, free_pages, block_table, cu, token_slots, pages_used)
+    _shaped("ctx", ctx, (R,))
+    if block_table.dim() != 2 or block_table.shape[0] != R:
+        raise ValueError("block_table must be [R, blocks]")
+    if cu is None:
+        cu = torch.empty(R + 1, dtype=torch.int32, device=dev)
+    if token_slots is None:
+        token_slots = torch.empty(rows, dtype=torch.int64, device=dev)
+    if pages_used is None:
+        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
+    _shaped("cu", cu, (R + 1,))
+    _shaped("token_slots", token_slots, (rows,))
+    _shaped("pages_used", pages_used, (1,))
+    with _Call(dev, stream) as st:
+        _check(kda_block_map(_ptr(lens), _ptr(ctx), _ptr(free_pages), free_pages.numel(), _ptr(block_table),
+                             block_table.shape[1], page_size, _ptr(cu), _ptr(token_slots), _ptr(pages_used), R, rows, st),
+               "kda_block_map")
+    return cu, token_slots, pages_used
+
+
+def _conv_weights(x, w, bias, state, C):
+    _typed(x.dtype, w=w, bias=bias, state=state)
+    _on(x.device, w, bias, state)
+    if w.dim() != 2 or w.shape[0] != C:
+        raise ValueError("w must be [C, K]")
+    K = w.shape[1]
+    _shaped("bias", bias, (C,))
+    if state is not None:
+        _shaped("state", state, (state.shape[0], K - 1, C))
+    return K
+
+
+def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, silu=True, head_dim=0, l2norm=False,
+               head_major=False, eps=1e-6, y=None, stream=None):
+    """Short causal convolution of prompts with Swish and the L2 norm of each
+    head (kda_short_conv).  x: [rows, C] with offsets cu [R + 1] int32 (None: one
+    sequence), or [B, T, C]; w: [C, K]; bias: [C]; state: pool [n_slots, K - 1, C],
+    updated in place; slots, ctx: [R] int32.  Returns y like x, or with
+    head_major [B, C // head_dim, T, head_dim], which chunk_fwd reads."""
+    import torch
+    lead = x.dim() - 1
+    if lead not in (1, 2):
+        raise ValueError("x must be [rows, C] or [B, T, C]")
+    C = x.shape[-1]
+    R, rows = _requests(x, lead, state, slots, ctx, cu)
+    K = _conv_weights(x, w, bias, state, C)
+    _on(x.device, slots, ctx, cu, y)
+    xs = _rows("x", x, lead)
+    if head_major:
+        if head_dim <= 0 or C % head_dim:
+            raise ValueError("head_major needs a head_dim that divides C")
+        shape = (R, C // head_dim, rows // max(R, 1), head_dim)
+    else:
+        shape = x.shape
+    if y is None:
+        y = torch.empty(shape, dtype=x.dtype, device=x.device)
+    _typed(x.dtype, y=y)
+    _shaped("y", y, shape)
+    if head_major:
+        _ptr(y)  # dense
+        ys = C
+    else:
+        ys = _rows("y", y, lead)
+    flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0) | (KDA_CONV_HEAD_MAJOR if head_major else 0)
+    with _Call(x.device, stream) as st:
+        _check(kda_short_conv(x.data_ptr(), xs, _ptr(w), _ptr(bias), _ptr(state), 0 if state is None else state.shape[0],
+                              _ptr(slots), _ptr(ctx), _ptr(cu), y.data_ptr(), ys, R, rows, C, K, head_dim,
+                              _dtype_code(x), flags, float(eps), st), "kda_short_conv")
+    return y
+
+
+def short_conv_step(x, w, state, bias=None, *, slots=None, silu=True, head_dim=0, l2norm=False, eps=1e-6, y=None,
+                    stream=None):
+    """short_conv for one new token of each of R sequences: x [R, C]; state: pool
+    [n_slots, K - 1, C], shifted in place.  Returns y [R, C]."""
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [R, C]")
+    R, C = x.shape
+    K = _conv_weights(x, w, bias, state, C)
+    _typed(torch.int32, slots=slots)
+    _shaped("slots", slots, (R,))
+    _on(x.device, slots, y)
+    xs = _rows("x", x, 1)
+    if y is None:
+        y = torch.empty(R, C, dtype=x.dtype, device=x.device)
+    _typed(x.dtype, y=y)
+    _shaped("y", y, (R, C))
+    flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0)
+    with _Call(x.device, stream) as st:
+        _check(kda_short_conv_step(x.data_ptr(), xs, _ptr(w), _ptr(bias), _ptr(state), state.shape[0], _ptr(slots),
+                                   y.data_ptr(), _rows("y", y, 1), R, C, K, head_dim, _dtype_code(x), flags, float(eps),
+                                   st), "kda_short_conv_step")
+    return y
+
+
+def _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead):
+    """(H, G, N, P, row strides) after the checks of shapes, types and devices."""
+    import torch
+    H, P = x.shape[-2:]
+    G, N = B.shape[-2:]
+    _typed(x.dtype, dt=dt, B=B, C=C)
+    _typed(torch.float32, A=A, D=D, dt_bias=dt_bias, state=state)
+    _on(x.device, dt, A, B, C, D, dt_bias, state)
+    _shaped("dt", dt, x.shape[:-1])
+    _shaped("B", B, x.shape[:lead] + (G, N))
+    _shaped("C", C, B.shape)
+    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
+        _shaped(name, t, (H,))
+    if state is not None:
+        _shaped("state", state, (state.shape[0], H, N, P))
+    return H, G, N, P, _rows("x", x, lead), _rows("dt", dt, lead), _rows("B", B, lead), _rows("C", C, lead)
+
+
+def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None, slots=None, ctx=None, cu=None,
+             block_table=None, pages=None, page_size=0, y=None, workspace=None, stream=None):
+    """Selective state space scan of prompts (kda_ssm_scan): S_t = exp(d A) S + d B x^T,
+    y = S^T C + D x with d = softplus(dt + dt_bias).  x: [rows, H, P] with offsets
+    cu [R + 1] int32 (None: one sequence), or [B, T, H, P]; dt [.., H]; B, C
+    [.., G, N]; A, D, dt_bias [H] fp32; state: pool [n_slots, H, N, P] fp32,
+    updated in place; slots, ctx [R] int32.  page_size > 0: the state at every
+    multiple of it goes to pages [n_pages, H, N, P] through block_table
+    [R, blocks] int32.  Returns y like x."""
+    import torch
+    lead = x.dim() - 2
+    if lead not in (1, 2):
+        raise ValueError("x must be [rows, H, P] or [B, T, H, P]")
+    R, rows = _requests(x, lead, state, slots, ctx, cu)
+    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead)
+    code = _dtype_code(x)
+    _on(x.device, slots, ctx, cu, block_table, pages, y, workspace)
+    stride = n_pages = 0
+    if page_size:
+        if block_table is None or pages is None:
+            raise ValueError("page_size needs block_table and pages")
+        _typed(torch.int32, block_table=block_table)
+        _typed(torch.float32, pages=pages)
+        if block_table.dim() != 2 or block_table.shape[0] != R:
+            raise ValueError("block_table must be [R, blocks]")
+        n_pages, stride = pages.shape[0], block_table.shape[1]
+        _shaped("pages", pages, (n_pages, H, N, P))
+    if y is None:
+        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _typed(x.dtype, y=y)
+    _shaped("y", y, x.shape)
+    with _Call(x.device, stream) as st:
+        ws = kda_ssm_scan_workspace_size(R, rows, H, G, N, P, code)
+        if ws == (1 << 64) - 1:
+            raise KdaError(2, "kda_ssm_scan_workspace_size")
+        if ws > 0 and workspace is None:
+            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
+        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        _check(kda_ssm_scan(x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(A), B.data_ptr(), bs, C.data_ptr(), cs, _ptr(D),
+                            _ptr(dt_bias), 1 if softplus else 0, _ptr(state), 0 if state is None else state.shape[0],
+                            _ptr(slots), _ptr(ctx), _ptr(cu), _ptr(block_table), stride, _ptr(pages), n_pages, page_size,
+                            y.data_ptr(), _rows("y", y, lead), R, rows, H, G, N, P, code, _ptr(workspace), wbytes, st),
+               "kda_ssm_scan")
+    return y
+
+
+def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, softplus=True, slots=None, y=None, stream=None):
+    """ssm_scan for one new token of each of R sequences: x [R, H, P], dt [R, H],
+    B, C [R, G, N]; state: pool [n_slots, H, N, P] fp32, updated in place.  Returns y [R, H, P]."""
+    import torch
+    if x.dim() != 3:
+        raise ValueError("x must be [R, H, P]")
+    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, 1)
+    R = x.shape[0]
+    _typed(torch.int32, slots=slots)
+    _shaped("slots", slots, (R,))
+    _on(x.device, slots, y)
+    if y is None:
+        y = torch.empty(R, H, P, dtype=x.dtype, device=x.device)
+    _typed(x.dtype, y=y)
+    _shaped("y", y, (R, H, P))
+    with _Call(x.device, stream) as st:
+        _check(kda_ssm_step(x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(A), B.data_ptr(), bs, C.data_ptr(), cs, _ptr(D),
+                            _ptr(dt_bias), 1 if softplus else 0, _ptr(state), state.shape[0], _ptr(slots), y.data_ptr(),
+                            _rows("y", y, 1), R, H, G, N, P, _dtype_code(x), st), "kda_ssm_step")
     return y

@@ -343,6 +343,161 @@ kda_status_t kda_chunk_fwd_noalloc(const void *q, const void *k, const void *v, 
 /* Size in bytes of the fixed scratch array kda_chunk_fwd_noalloc uses. */
 size_t kda_noalloc_scratch_bytes(void);
 
+/*
+ * Packed requests: the serving form of the layer around the recurrence.
+ *
+ * The calls below work on R sequences ("requests") whose tokens lie one after
+ * another in the rows of token-major arrays, and whose states lie in a pool.
+ * They share these arguments:
+ *   R, rows  : sequences, and rows of the token-major arrays
+ *   cu       : [R + 1] int32, non-decreasing; sequence r owns rows cu[r] ..
+ *              cu[r + 1] - 1 (none is allowed), and cu[R] <= rows.  Rows before
+ *              cu[0] and from cu[R] on belong to no sequence and are neither
+ *              read nor written.  NULL: R sequences of rows / R tokens each
+ *              (rows % R == 0, else KDA_ERR_SHAPE).
+ *   ctx      : [R] int32, tokens that each sequence has behind it already; a
+ *              sequence with ctx[r] <= 0 starts from a zero state, others from
+ *              their pool entry.  NULL: all start from zero.
+ *   slots    : [R] int32, each sequence's entry in the pool; NULL: entry r.  A
+ *              negative slot marks a padded request: its rows of the output and
+ *              the pool stay as they were.  The non-negative slots of a call
+ *              are distinct (a repeated one leaves that entry, and the outputs
+ *              of the sequences that name it, undefined).
+ *   state, n_slots : the pool and its number of entries, or NULL and 0: every
+ *              sequence starts from zero and nothing is saved.  The entry of a
+ *              sequence that has tokens is overwritten with its new state; of
+ *              one without tokens it stays as it was.
+ *   strides  : in elements, between consecutive rows; inside a row elements are
+ *              dense.  Token-major arrays need only be aligned to their element
+ *              size; rows that are 16-byte aligned (base and stride) are faster.
+ * cu, ctx, slots and the tables are read on the device, so a call needs no
+ * copy of them on the host and can be captured into a CUDA graph and replayed
+ * on new lengths.  Values that would lead outside a buffer (a slot of n_slots
+ * or more, cu[R] > rows, a block of n_pages or more) are not followed: that
+ * sequence or row is skipped and KDA_ERR_DEVICE recorded
+ * (kda_get_device_status).  cu, ctx, slots: 4-byte aligned.  Outputs must not
+ * overlap each other or any input.
+ */
+
+/*
+ * Block tables and token slots from request lengths, on the device (the paged
+ * pool of Kimi K3 report, section 5.4.1).  One launch:
+ *   cu[r + 1]     = len[0] + .. + len[r],  cu[0] = 0
+ *   block_table   : request r, which has ctx[r] tokens in its first
+ *                   ceil(ctx[r] / page_size) blocks, gets the blocks up to
+ *                   ceil((ctx[r] + len[r]) / page_size): its row receives the next
+ *                   entries of free_pages, requests in order, blocks in order.
+ *                   Entries of the row that are not new stay as they were.
+ *   token_slots   : of the token in row i of request r, at position
+ *                   p = ctx[r] + i - cu[r]: block_table[r][p / page_size] * page_size
+ *                   + p % page_size;  -1 for rows from cu[R] on, and where the table
+ *                   holds no block (a negative entry, or a position behind its end)
+ *   pages_used[0] = blocks that the call hands out.  Where that exceeds n_free, the
+ *                   blocks behind the last free one are -1: the caller compares.
+ *
+ *   len, ctx    : [R] int32 (negative: 0); ctx may be NULL (all 0)
+ *   free_pages  : [n_free] int32, not changed; may be NULL when n_free is 0
+ *   block_table : [R, table_stride] int32, updated in place
+ *   cu          : [R + 1] int32;  token_slots : [rows] int64 (8-byte aligned);  pages_used : [1] int32
+ *   R           : at most 16384 (KDA_ERR_SHAPE beyond);  page_size >= 1
+ * If the lengths add up to more than rows, cu holds the sums (saturated at
+ * 2^31 - 1) and token_slots the first rows tokens' slots.
+ */
+kda_status_t kda_block_map(const int *len, const int *ctx, const int *free_pages, int n_free, int *block_table,
+                           int table_stride, int page_size, int *cu, int64_t *token_slots, int *pages_used, int R,
+                           int rows, kda_stream_t stream);
+
+/* Bits of `flags` of the short convolutions. */
+enum {
+  KDA_CONV_SILU = 1,      /* y = v Sigmoid(v) (Swish) */
+  KDA_CONV_L2NORM = 2,    /* after it, every head divided by sqrt(sum of squares + eps) */
+  KDA_CONV_HEAD_MAJOR = 4 /* y is [R, C / head_dim, T, head_dim] instead of token-major */
+};
+
+/*
+ * Short causal convolution of prompts: the input edge of a KDA layer (Kimi K3
+ * report, section 2.1.1, Eq. 2: q, k = L2Norm(Swish(ShortConv(W x))),
+ * v = Swish(ShortConv(W_v x)), without the projections), and of a selective
+ * state space layer.  Per sequence and channel c, at position t of the sequence
+ *     v_t = bias[c] + sum_{i=0}^{K-1} w[c][i] u[t - (K - 1) + i],
+ * u being the channel's inputs, u[-1], .., u[-(K - 1)] those before the call
+ * (from the pool, or zeros), then Swish and the L2 norm as `flags` say.
+ *   x       : token-major [rows, C] dtype, x_stride >= C
+ *   w, bias : [C, K] and [C] dtype; bias may be NULL (zeros)
+ *   state   : pool [n_slots, K - 1, C] dtype: a sequence's last K - 1 inputs, oldest first
+ *   y       : token-major [rows, C] dtype with y_stride >= C, or with
+ *             KDA_CONV_HEAD_MAJOR [R, C / head_dim, rows / R, head_dim] dtype, dense:
+ *             what kda_chunk_fwd reads as q, k or v (y_stride ignored; cu must be NULL)
+ *   head_dim: one of 16, 32, 64, 128 dividing C with KDA_CONV_L2NORM or
+ *             KDA_CONV_HEAD_MAJOR; ignored otherwise
+ *   eps     : of the norm; finite, >= 0
+ *   K       : 2, 3 or 4 taps
+ * Sums are fp32 and rounded once.
+ */
+kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *w, const void *bias, void *state, int n_slots,
+                            const int *slots, const int *ctx, const int *cu, void *y, int64_t y_stride, int R, int rows,
+                            int C, int K, int head_dim, kda_dtype_t dtype, int flags, float eps, kda_stream_t stream);
+
+/*
+ * The same for one new token of each of R sequences: every pool entry is
+ * shifted by one input in place.  x : [R, C] with x_stride; y : [R, C] with
+ * y_stride (KDA_CONV_HEAD_MAJOR is the same layout: [R, C / head_dim, head_dim]).
+ * state must not be NULL.
+ */
+kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w, const void *bias, void *state,
+                                 int n_slots, const int *slots, void *y, int64_t y_stride, int R, int C, int K,
+                                 int head_dim, kda_dtype_t dtype, int flags, float eps, kda_stream_t stream);
+
+/*
+ * Selective state space scan of prompts: the recurrence of kda_chunk_fwd
+ * without the erase term, with one decay for a head (the scalar-gate relative
+ * of Kimi K3 report, section 2.1.1, Eq. 1).  Per sequence and head h a state
+ * S in R^{N x P}:
+ *     d_t = softplus(dt_t + dt_bias[h])        (d_t = dt_t + dt_bias[h] if softplus is 0)
+ *     S_t = exp(d_t A[h]) S_{t-1} + d_t B_t x_t^T,      y_t = S_t^T C_t + D[h] x_t
+ * B and C are shared by the H / G heads of a group (head h reads group h / (H / G)).
+ *   x   : [rows, H, P] dtype, row stride x_stride;   dt : [rows, H] dtype, dt_stride
+ *   Bm, Cm : [rows, G, N] dtype, row strides b_stride, c_stride
+ *   A   : [H] fp32, <= 0;   D, dt_bias : [H] fp32, or NULL (zeros)
+ *   state  : pool [n_slots, H, N, P] fp32, 16-byte aligned
+ *   y   : [rows, H, P] dtype, y_stride
+ *   H % G == 0;  N, P : each one of 16, 32, 64, 128
+ * d_t A[h] <= 0 is relied on (d_t >= 0, which softplus gives).  State,
+ * decays and sums are fp32; on the tensor-core path (bf16) products take bf16
+ * operands as noted at the kernel.
+ *
+ * State snapshots (section 5.4.1): with page_size > 0 (a multiple of 128) the
+ * state after every position that is a multiple of page_size (counted with
+ * ctx) is written to pages[block_table[r][position / page_size - 1]]:
+ *   block_table : [R, table_stride] int32 (kda_block_map makes it); a negative
+ *                 entry, or a block behind the table's end: not written
+ *   pages       : [n_pages, H, N, P] fp32, 16-byte aligned
+ * page_size 0: none, and the three are ignored.
+ *
+ * workspace   : device scratch of kda_ssm_scan_workspace_size(...) bytes, 16-byte
+ *               aligned (NULL when that is 0); contents on entry are ignored.  Calls that
+ *               may overlap need one each.
+ */
+kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
+                          const void *Bm, int64_t b_stride, const void *Cm, int64_t c_stride, const float *D,
+                          const float *dt_bias, int softplus, float *state, int n_slots, const int *slots,
+                          const int *ctx, const int *cu, const int *block_table, int table_stride, float *pages,
+                          int n_pages, int page_size, void *y, int64_t y_stride, int R, int rows, int H, int G, int N,
+                          int P, kda_dtype_t dtype, void *workspace, size_t workspace_bytes, kda_stream_t stream);
+
+/* Workspace bytes of kda_ssm_scan (0 if none, (size_t)-1 on invalid sizes). */
+size_t kda_ssm_scan_workspace_size(int R, int rows, int H, int G, int N, int P, kda_dtype_t dtype);
+
+/*
+ * The same for one new token of each of R sequences, states updated in place:
+ * x, y : [R, H, P], dt : [R, H], Bm, Cm : [R, G, N] dtype with row strides;
+ * state : pool [n_slots, H, N, P] fp32, 16-byte aligned, not NULL.
+ */
+kda_status_t kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
+                          const void *Bm, int64_t b_stride, const void *Cm, int64_t c_stride, const float *D,
+                          const float *dt_bias, int softplus, float *state, int n_slots, const int *slots, void *y,
+                          int64_t y_stride, int R, int H, int G, int N, int P, kda_dtype_t dtype, kda_stream_t stream);
+
 /* Human-readable name of a status code (static string, never NULL). */
 const char *kda_status_string(kda_status_t s);
 
