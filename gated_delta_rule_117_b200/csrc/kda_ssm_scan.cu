@@ -192,6 +192,7 @@ size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16)
 
 cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st) {
   const int seg = simt_segment(a.q.R, a.q.rows, a.H);
+  if (ssm_tc_fits(a)) return launch_ssm_tc(a, seg, st);
 #define KDA_SSM_CASE(NN, PP)    \
   if (a.N == NN && a.P == PP)   \
     return a.bf16 ? launch_t<NN, PP, __nv_bfloat16>(a, seg, st) : launch_t<NN, PP, float>(a, seg, st);

@@ -65,6 +65,10 @@ inline size_t seg_workspace(int64_t items, int H, int N, int P) {
 }
 cudaError_t launch_segment_states(const SsmArgs &a, int seg, cudaStream_t st);
 
+// The tensor-core scan (bf16, 16-byte aligned rows), and whether a call's arrays fit it.
+bool ssm_tc_fits(const SsmArgs &a);
+cudaError_t launch_ssm_tc(const SsmArgs &a, int seg, cudaStream_t st);
+
 // Time step d and the pool entry of a snapshot, shared by the scan kernels.
 template <typename T>
 __device__ __forceinline__ float time_step(const SsmArgs &a, int64_t row, int h) {
