@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
         y += __shfl_xor_sync(~0u, y, 2);
         if (quarter == 0) sy[t][p] = fmaf(skip, xv, y);
         if (a.page)
-          if (float *to = snapshot(a, it.r, h, (int64_t)it.s.ctx + t0 + t + 1, tell)) save(to);
+          if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(t0 + t + 1), tell)) save(to);
       }
     }
     if (kOut) {

@@ -76,11 +76,11 @@ __device__ __forceinline__ float time_step(const SsmArgs &a, int64_t row, int h)
   return a.softplus ? softplus(d) : d;
 }
 
-// Snapshot of sequence r after `pos` tokens (counted with ctx): its place, or null.
-__device__ __forceinline__ float *snapshot(const SsmArgs &a, int r, int h, int64_t pos, bool tell) {
-  if (a.page == 0 || pos % a.page != 0) return nullptr;
-  const int64_t j = pos / a.page - 1;
-  if (j < 0 || j >= a.table_stride) return nullptr;
+// Snapshot of sequence r after `pos` tokens (counted with ctx, so below 2^32): its place, or null.
+__device__ __forceinline__ float *snapshot(const SsmArgs &a, int r, int h, uint32_t pos, bool tell) {
+  if (a.page == 0 || pos % (uint32_t)a.page != 0) return nullptr;
+  const uint32_t j = pos / (uint32_t)a.page - 1;  // (pos 0 gives a block behind every table)
+  if (j >= (uint32_t)a.table_stride) return nullptr;
   const int p = a.table[(int64_t)r * a.table_stride + j];
   if (p < 0) return nullptr;
   if (p >= a.n_pages) {

@@ -7,7 +7,7 @@
 // so a chunk is four products (M x N x K):
 //     G  = C B^T      128 x 128 x N      scores
 //     Yx = C S        128 x 64 x N       what the entering state gives
-//     dS = B^T wx     128 x 64 x 128     (wx = d 2^{L_127 - L} x, as bf16 hi + lo)
+//     dS = B^T wx     128 x 64 x 128     (wx = d 2^{L_127 - L} x, in three bf16 terms)
 //     Yi = W x        128 x 64 x 128     (W = G masked and decayed, A operand in TMEM)
 // Every exponent is a sum of l over consecutive tokens, formed from sums inside
 // blocks of 32 tokens and whole-block totals, never as a difference of long
@@ -16,22 +16,30 @@
 // row and a column part, so exponentials are taken for the diagonal blocks only.
 //
 // Rounding.  The state lives in fp32 registers; what is added to it is split into
-// bf16 hi + lo (16 bits), as one bf16 would put 2^-9 of every update into it for
-// good.  W and the copy of S that outputs read are single bf16: each costs an
-// output about what its own rounding to bf16 does, and nothing carries on.
+// three bf16 terms (24 bits), so the state keeps fp32 accuracy: one bf16 would put
+// 2^-9 of every update into it for good, and two leave 3e-6.  W and the copy of S
+// that outputs read are single bf16: each costs an output less than its own
+// rounding to bf16 does, and nothing carries on.
 //
-// What bounds it: 1.5 K cycles of tensor-core work a chunk against 32 KB of x and
-// y from HBM (0.74 us at the copy rate); the roles below overlap, so the tensor
-// pipe's 0.8 us and the handovers between roles set the pace.
+// What bounds it: 1.8 K cycles of tensor-core work a chunk (0.95 us) against 32 KB
+// of x and y from HBM (0.74 us at the copy rate), and the handovers below.
 //
-// Work split: one CTA a (segment, head, 64 columns of P), 16 warps:
-//   warp 0     producer: TMA loads of C, B, x (two stages), TMA stores of y
-//   warp 1     decays: d, sums of l, the factors of every role (two stages)
-//   warp 2     issues every MMA
-//   warps 4-7  scores: thread t owns row t of G; writes W to TMEM
-//   warps 8-11 tokens: thread t owns row t of x; writes wx, later the output row
-//   warps 12-15 state: thread n owns row n of S (64 fp32 registers); writes the
-//              bf16 copy, the snapshots and the final state
+// Work split: one CTA a (segment, head, 64 columns of P), 32 warps of 64 registers:
+//   warp 0       producer: TMA loads of B, x (two stages) and C
+//   warps 1, 3   decays: steps, sums of l, the factors of every role (up to four
+//                chunks ahead)
+//   warp 2       issues every MMA
+//   warps 4-11   scores: two threads own row t of G, half a block of columns each;
+//                they write W to TMEM
+//   warps 12-15  tokens: thread t writes row t of wx
+//   warps 16-23  state: two threads own row n of S, 32 columns (fp32 registers)
+//                each; they write the bf16 copy, the snapshots and the final state
+//   warps 24-31  outputs: two threads own row t of y, 32 columns each; a warp stores
+//                its tile by TMA
+// The order of a chunk's products lets each role work under the others' tensor
+// time: scores under Yx and dS, the state update under Yi and the next G.  C is
+// single-buffered (its last reader, Yx, comes early), which makes room for wx's
+// third term; B and x have two stages.
 // Columns of S are independent, so P = 128 is two CTAs (which form G twice: it
 // is a third of the tensor work and saves any exchange).  Rows behind a chunk's
 // last token are zeroed in the operands that sum over tokens, and not stored;
@@ -53,58 +61,57 @@ using namespace sm100;
 
 constexpr int Q = 128;    // tokens of a chunk
 constexpr int PC = 64;    // state columns of a CTA
-constexpr int NT = 512;
+constexpr int NT = 1024;
 static_assert(Q == kAlign, "snapshots fall on chunk ends");
 
 // ---- shared memory (byte offsets from a 1024-aligned base) -------------------
 // Tiles of 128-byte rows in the 128-byte swizzle; [rows x 128] tiles are two
 // blocks of 64 columns (16 KB each).
-constexpr int kC = 0;              // [2] C, 32 KB
-constexpr int kB = 65536;          // [2] B, 32 KB
-constexpr int kX = 131072;         // [2] x, 16 KB; later the chunk's y
-constexpr int kW = 163840;         // wx hi | lo, 16 KB each
-constexpr int kS = 196608;         // S as bf16 [n][p], 16 KB
-constexpr int kDec = 212992;       // [2] Decays
-constexpr int kBarOff = 219264;
-constexpr int kMisc = 219520;       // TMEM base address, abort flag
-constexpr int kSmemBytes = 219584 + 1024;
+constexpr int kC = 0;              // C, 32 KB
+constexpr int kB = 32768;          // [2] B, 32 KB
+constexpr int kX = 98304;          // [2] x, 16 KB
+constexpr int kW = 131072;         // wx terms, 3 x 16 KB
+constexpr int kS = 180224;         // S as bf16 [n][p], 16 KB
+constexpr int kY = 196608;         // y, 16 KB
+constexpr int kDec = 212992;       // [4] Decays
+constexpr int kBarOff = 225536;
+constexpr int kMisc = 225792;      // Misc
+constexpr int kSmemBytes = 225920 + 1024;
 
 struct Decays {
   float d[Q];        // step (0 behind the last token)
   float pre[Q];      // sum of l from the token's block's first token to the token
-  float w[Q];        // d 2^(sum of l behind the token, to the chunk's end)
+  float w[Q];        // d 2^(sum behind the token to the chunk's end)
   float col[3][Q];   // d 2^(sum behind the token to the start of the block i + 1, i + 2, i + 3 of its own i)
+  float total[4];    // sum of l of each block
   float before[4];   // 2^(sum of l of the blocks before block i)
   float all;         // 2^(sum of l of the chunk)
   float pad[3];
 };
-static_assert(kDec + 2 * sizeof(Decays) <= kBarOff && kSmemBytes <= 232448, "shared memory layout");
+static_assert(kDec + 4 * sizeof(Decays) <= kBarOff && kSmemBytes <= 232448, "shared memory layout");
 
 enum {
-  F_CB = 0,   // [2] C and B landed
-  F_X = 2,    // [2] x landed
-  DEC = 4,    // [2] decays written
-  DEC_FREE = 6,  // [2] decays read by every role
-  G_DONE = 8, // G in TMEM
+  F_BX = 0,   // [2] B and x landed
+  BX_FREE = 2,   // [2] every reader of B and x is done
+  DEC = 4,       // [4] decays written
+  DEC_FREE = 8,  // [4] decays read by the other roles
+  F_C = 12,   // C landed
+  C_FREE,     // C read (Yx done)
+  G_DONE,     // G in TMEM
   W_READY,    // W in TMEM (and G read)
-  WX_READY,   // wx written, tail rows zeroed
+  WX_READY,   // wx written, tail rows zeroed; the dS before is read
   DS_DONE,    // dS in TMEM (and wx and S read)
-  DS_READ,    // dS read
-  S_READY,    // bf16 S of the chunk written
+  YX_READY,   // bf16 S of the chunk written; the Yi and Yx before are read
   Y_DONE,     // [2] Yi and Yx in TMEM (and W read)
-  Y_READ = Y_DONE + 2,  // [2] they are read
-  CB_FREE = Y_READ + 2, // [2] every MMA of the chunk done: C and B may be replaced
-  X_FREE = CB_FREE + 2, // [2] x read (y staged in its place, in output runs)
-  DRAIN = X_FREE + 2,   // every MMA issued is done
+  TOTALS = Y_DONE + 2,  // the blocks' totals are written
+  DRAIN,      // every MMA issued is done
   BARS
 };
 static_assert(kBarOff + 8 * BARS <= kMisc, "barriers");
 
 // TMEM columns
 constexpr uint32_t kCols = 512;
-constexpr uint32_t tG = 0, tW = 128, tDS = 192;
-__device__ __forceinline__ uint32_t tYi(int i) { return 256u + 128u * (i & 1); }
-__device__ __forceinline__ uint32_t tYx(int i) { return tYi(i) + 64u; }
+constexpr uint32_t tG = 0, tW = 128, tDS = 192, tYi = 384, tYx = 448;  // dS: one block of 64 for each term of wx
 
 struct TcArgs {
   SsmArgs a;
@@ -113,36 +120,53 @@ struct TcArgs {
   uint64_t wait_ns;
 };
 
+// What a wait needs when it does not succeed at once (shared memory).
+struct Misc {
+  uint32_t tmem;
+  volatile int abort;
+  unsigned *status;
+  uint64_t wait_ns;
+};
+
+// One copy of the wait for every role: the roles' hot loops together should fit
+// the SM's instruction cache (unrolled and inlined to 108 KB, the kernel spent a
+// third of its time waiting for instructions, and more on the SMs that share a
+// larger cache level with others).  The whole warp calls it and gets the same
+// answer, as warp-wide instructions follow.
+__device__ __noinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *m) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (__all_sync(~0u, ok)) return true;
+  if (!ok) {
+    const uint64_t t0 = global_ns();
+    for (;;) {
+      if ((ok = mbar_try_wait_sleep(bar, parity, 1000000u))) break;
+      if (m->abort) break;
+      if (global_ns() - t0 > m->wait_ns) {
+        m->abort = 1;
+        atomicExch(m->status, kDevTimeout);
+        break;
+      }
+    }
+  }
+  return __all_sync(~0u, ok);
+}
+
 struct Cta {
   unsigned char *sm;
   uint64_t *bar;
-  volatile int *abort;
-  unsigned *status;
-  uint64_t wait_ns;
+  Misc *m;
 
-  __device__ __noinline__ bool wait_slow(int b, uint32_t parity) const {
-    const uint64_t t0 = global_ns();
-    for (;;) {
-      if (mbar_try_wait_sleep(&bar[b], parity, 1000000u)) return true;
-      if (*abort) return false;
-      if (global_ns() - t0 > wait_ns) break;
-    }
-    *abort = 1;
-    atomicExch(status, kDevTimeout);
-    return false;
-  }
-  // Phase `k` (0, 1, ...) of barrier b; the whole warp calls it.
-  __device__ __forceinline__ bool wait(int b, int k) const {
-    // the same answer for the whole warp: warp-wide instructions follow
-    bool ok = mbar_try_wait(&bar[b], k & 1);
-    if (__all_sync(~0u, ok)) return true;
-    ok = ok || wait_slow(b, k & 1);
-    return __all_sync(~0u, ok);
-  }
+  // Phase `k` (0, 1, ...) of barrier b.
+  __device__ __forceinline__ bool wait(int b, int k) const { return wait_bar(&bar[b], k & 1, m); }
   // Phase k / 2 of entry k % 2 of a ring.
-  __device__ __forceinline__ bool wait2(int b, int k) const { return wait(b + (k & 1), k >> 1); }
-  __device__ __forceinline__ void arrive(int b) const { mbar_arrive(&bar[b]); }
-  __device__ __forceinline__ Decays &dec(int i) const { return *reinterpret_cast<Decays *>(sm + kDec + (i & 1) * sizeof(Decays)); }
+  __device__ __forceinline__ bool wait2(int b, int k) const { return wait_bar(&bar[b + (k & 1)], (k >> 1) & 1, m); }
+  // One arrival for the warp, after what all its lanes did before.
+  __device__ __forceinline__ void arrive(int b) const {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&bar[b]);
+  }
+  __device__ __forceinline__ bool wait4(int b, int k) const { return wait_bar(&bar[b + (k & 3)], (k >> 2) & 1, m); }
+  __device__ __forceinline__ Decays &dec(int i) const { return *reinterpret_cast<Decays *>(sm + kDec + (i & 3) * sizeof(Decays)); }
 };
 
 // Chunk i of an item: its first token (counted from the sequence's first) and its tokens.
@@ -162,17 +186,42 @@ struct Chunks {
 
 __device__ __forceinline__ float4 f4(const float *p) { return *reinterpret_cast<const float4 *>(p); }
 
-// v as bf16 hi + lo: returns packed hi (rounded), writes packed lo.
-__device__ __forceinline__ uint32_t split(float2 v, uint32_t &lo) {
-  const __nv_bfloat162 h = __float22bfloat162_rn(v);
-  const float2 b = __bfloat1622float2(h);
-  lo = pack_bf16x2(v.x - b.x, v.y - b.y);
-  return *reinterpret_cast<const uint32_t *>(&h);
+// 2^v.  The hardware's approximation (2^-22 relative); results below the normal range are 0.
+__device__ __forceinline__ float ex2(float v) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// log(1 + e^v) = max(v, 0) + log1p(z), z = e^-|v|, by log1p(z) = 2 atanh(z / (2 + z)):
+// the argument is at most 1/3, where seven terms of the series s + s^3 / 3 + ... leave 2e-8.
+// Four times shorter than log1pf(expf(v)), which the decay warps feel.
+__device__ __forceinline__ float softplus_fast(float v) {
+  const float z = __expf(-fabsf(v)), s = __fdividef(z, 2.f + z), q = s * s;
+  float r = fmaf(q, 1.f / 13.f, 1.f / 11.f);
+  r = fmaf(q, r, 1.f / 9.f);
+  r = fmaf(q, r, 1.f / 7.f);
+  r = fmaf(q, r, 1.f / 5.f);
+  r = fmaf(q, r, 1.f / 3.f);
+  r = fmaf(q * r, s, s);
+  return fmaxf(v, 0.f) + 2.f * r;
+}
+
+__device__ __forceinline__ float2 unpack(uint32_t u) {
+  return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// The next bf16 term of v: returns it packed and leaves the exact remainder in v.
+__device__ __forceinline__ uint32_t take_term(float2 &v) {
+  const uint32_t h = pack_bf16x2(v.x, v.y);
+  v = __ffma2_rn(unpack(h), make_float2(-1.f, -1.f), v);
+  return h;
 }
 
 // kOut: the run that writes y, snapshots and final states; else the state pass,
 // which leaves each segment's S~ and decay in the workspace.
-template <bool kOut>
+// NK: K steps over N (N / 16).
+template <bool kOut, int NK>
 __global__ void __launch_bounds__(NT, 1)
     ssm_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
                   const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my, const TcArgs p) {
@@ -186,405 +235,456 @@ __global__ void __launch_bounds__(NT, 1)
   if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const Chunks ch(it);
-  const int n = ch.n, g = h / (a.H / a.G), nk = a.N / 16;
+  const int n = ch.n, g = h / (a.H / a.G);
 
   Cta x;
   unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   x.sm = sm;
   x.bar = reinterpret_cast<uint64_t *>(sm + kBarOff);
-  x.abort = reinterpret_cast<volatile int *>(sm + kMisc + 4);
-  x.status = a.q.status;
-  x.wait_ns = p.wait_ns;
-  uint32_t *tslot = reinterpret_cast<uint32_t *>(sm + kMisc);
+  x.m = reinterpret_cast<Misc *>(sm + kMisc);
   const uint32_t sbase = smem_u32(sm);
   if (tid == 0) {
     for (int i = 0; i < BARS; ++i) {
-      uint32_t count = 1;  // TMA and MMA completions
-      if (i == DEC || i == DEC + 1) count = 32;
-      if (i == DEC_FREE || i == DEC_FREE + 1) count = kOut ? 384 : 256;
-      if (i == W_READY || i == WX_READY || i == DS_READ || i == S_READY || i == Y_READ || i == Y_READ + 1 ||
-          i == X_FREE || i == X_FREE + 1)
-        count = 128;
+      uint32_t count = 1;  // TMA and MMA completions; the others count warps
+      if (i == BX_FREE || i == BX_FREE + 1) count = kOut ? 9 : 1;  // the MMAs, and the output warps
+      if (i >= DEC && i < DEC + 4) count = 2;
+      if (i >= DEC_FREE && i < DEC_FREE + 4) count = kOut ? 28 : 12;
+      if (i == TOTALS) count = 2;
+      if (i == W_READY) count = 8;
+      if (i == WX_READY) count = 12;  // token and state warps
+      if (i == YX_READY) count = 16;  // state and output warps
       mbar_init(&x.bar[i], count);
     }
-    *x.abort = 0;
+    x.m->abort = 0;
+    x.m->status = a.q.status;
+    x.m->wait_ns = p.wait_ns;
     mbar_init_fence();
   }
   if (warp == 3) {
-    tmem_alloc(tslot, kCols);
+    tmem_alloc(&x.m->tmem, kCols);
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb = *tslot;
+  const uint32_t tb = x.m->tmem;
   const uint32_t tl = tb + ((uint32_t)(32 * (warp & 3)) << 16);  // this warp's lanes
+  const int t = 32 * (warp & 3) + lane;  // this thread's row in its role
   const int row_of_seq = it.s.start;
 
   if (warp == 0) {
     // ======================= producer =======================
-    const uint32_t cb_bytes = (kOut ? 2u : 1u) * (a.N > 64 ? 32768u : 16384u);
-    int cb = 0, xs = 0;  // loads issued
+    const uint32_t half = NK > 4 ? 32768u : 16384u;  // bytes of a B or C tile that are loaded
+    int loads = 0, cloads = 0;
     bool ok = true;
-    auto store = [&](int i) {  // y of chunk i, staged in its x tile (ragged chunks are stored by the token warps)
-      if (kOut && ch.count(i) == Q) {
-        tma_store_3d_warp(&my, sm + kX + (i & 1) * 16384, p0, h, row_of_seq + ch.first(i));
-        bulk_commit_warp();
-        bulk_wait_read_all();
-        __syncwarp();
-      }
-    };
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1, row = row_of_seq + ch.first(i);
-      if (i >= 2 && !(ok = x.wait2(CB_FREE, i - 2))) break;
-      mbar_arrive_expect_tx_warp(&x.bar[F_CB + st], cb_bytes);
-      for (int c = 0; c < a.N; c += 64) {
-        if (kOut) tma_load_3d_warp(sm + kC + st * 32768 + c * 256, &mc, &x.bar[F_CB + st], c, g, row);
-        tma_load_3d_warp(sm + kB + st * 32768 + c * 256, &mb, &x.bar[F_CB + st], c, g, row);
+      if (i >= 2 && !(ok = x.wait2(BX_FREE, i - 2))) break;
+      mbar_arrive_expect_tx_warp(&x.bar[F_BX + st], half + 16384u);
+      tma_load_3d_warp(sm + kX + st * 16384, &mx, &x.bar[F_BX + st], p0, h, row);
+#pragma unroll 1
+      for (int c = 0; c < 16 * NK; c += 64)
+        tma_load_3d_warp(sm + kB + st * 32768 + c * 256, &mb, &x.bar[F_BX + st], c, g, row);
+      loads = i + 1;
+      if (kOut) {
+        if (i >= 1 && !(ok = x.wait(C_FREE, i - 1))) break;
+        mbar_arrive_expect_tx_warp(&x.bar[F_C], half);
+#pragma unroll 1
+        for (int c = 0; c < 16 * NK; c += 64) tma_load_3d_warp(sm + kC + c * 256, &mc, &x.bar[F_C], c, g, row);
+        cloads = i + 1;
       }
-      cb = i + 1;
-      if (i >= 2) {
-        if (!(ok = x.wait2(X_FREE, i - 2))) break;
-        store(i - 2);
+      if (i + 2 < n) {  // the chunk after the next on its way from HBM
+        const int next = row_of_seq + ch.first(i + 2);
+        tma_prefetch_3d_warp(&mx, p0, h, next);
+#pragma unroll 1
+        for (int c = 0; c < 16 * NK; c += 64) {
+          tma_prefetch_3d_warp(&mb, c, g, next);
+          if (kOut) tma_prefetch_3d_warp(&mc, c, g, next);
+        }
       }
-      mbar_arrive_expect_tx_warp(&x.bar[F_X + st], 16384u);
-      tma_load_3d_warp(sm + kX + st * 16384, &mx, &x.bar[F_X + st], p0, h, row);
-      xs = i + 1;
-    }
-    for (int i = max(0, n - 2); ok && i < n; ++i) {
-      if (!(ok = x.wait2(X_FREE, i))) break;
-      store(i);
     }
     if (!ok) {  // loads in flight must land before shared memory is given up
       const uint64_t t0 = global_ns();
-      for (int k = 0; k < 4; ++k) {
-        const int issued = k < 2 ? cb : xs, b = (k < 2 ? F_CB : F_X) + (k & 1);
-        const int last = issued - 1 - ((issued - 1 - (k & 1)) & 1);  // the last chunk of this stage
-        if (last < 0) continue;
-        while (!mbar_try_wait_sleep(&x.bar[b], (last >> 1) & 1, 1000000u))
+#pragma unroll 1
+      for (int k = max(0, loads - 2); k < loads; ++k)
+        while (!mbar_try_wait_sleep(&x.bar[F_BX + (k & 1)], (k >> 1) & 1, 1000000u))
           if (global_ns() - t0 > p.wait_ns) break;
-      }
+      if (cloads > 0)
+        while (!mbar_try_wait_sleep(&x.bar[F_C], (cloads - 1) & 1, 1000000u))
+          if (global_ns() - t0 > p.wait_ns) break;
     }
-  } else if (warp == 1) {
-    // ======================= decays =======================
-    const float A2 = a.A[h] * 1.4426950408889634f;
-    const __nv_bfloat16 *dt = (const __nv_bfloat16 *)a.dt + h;
-    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-    float raw[4];
-    auto fetch = [&](int i) {
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int t = 32 * b + lane;
-        raw[b] = i < n && t < ch.count(i) ? __bfloat162float(dt[(int64_t)(row_of_seq + ch.first(i) + t) * a.dt_stride]) : 0.f;
-      }
-    };
-    fetch(0);
-    float total = 0.f;
-    for (int i = 0; i < n; ++i) {
-      const int count = ch.count(i);
-      float d[4], pre[4], suf[4], L[4];
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        float v = raw[b] + bias;
-        if (a.softplus) v = softplus(v);
-        d[b] = 32 * b + lane < count ? v : 0.f;
-      }
-      fetch(i + 1);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const float l = d[b] * A2;
-        float up = l, dn = l;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const float u = __shfl_up_sync(~0u, up, o), v = __shfl_down_sync(~0u, dn, o);
-          if (lane >= o) up += u;
-          if (lane + o < 32) dn += v;
-        }
-        const float after = __shfl_down_sync(~0u, dn, 1);
-        pre[b] = up;
-        suf[b] = lane < 31 ? after : 0.f;
-        L[b] = __shfl_sync(~0u, up, 31);
-      }
-      if (i >= 2 && !x.wait2(DEC_FREE, i - 2)) break;
-      Decays &D = x.dec(i);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const int t = 32 * b + lane;
-        D.d[t] = d[b];
-        D.pre[t] = pre[b];
-        float s = suf[b];
-#pragma unroll
-        for (int k = b + 1; k < 4; ++k) {
-          D.col[k - b - 1][t] = d[b] * exp2f(s);
-          s += L[k];
-        }
-        D.w[t] = d[b] * exp2f(s);
-      }
-      const float all = L[0] + L[1] + L[2] + L[3];
-      total += all;
-      if (lane == 0) {
-        D.before[0] = 1.f;
-        D.before[1] = exp2f(L[0]);
-        D.before[2] = exp2f(L[0] + L[1]);
-        D.before[3] = exp2f(L[0] + L[1] + L[2]);
-        D.all = exp2f(all);
-      }
-      x.arrive(DEC + (i & 1));
-    }
-    if (!kOut && lane == 0 && p0 == 0) p.decays[it.item * a.H + h] = exp2f(total);
   } else if (warp == 2) {
     // ======================= MMA issue =======================
     const uint32_t idG = idesc_bf16(128, 128, false, false, false);
     const uint32_t idYx = idesc_bf16(128, 64, false, true, false);
-    const uint32_t idDS = idesc_bf16(128, 64, true, true, false);
+    const uint32_t idDS = idesc_bf16(128, 192, true, true, false);  // the terms of wx side by side
     const uint64_t dS = sdesc_sw128(sbase + kS, 16, 1024);
-    const uint64_t dW = sdesc_sw128(sbase + kW, 16, 1024);
+    const uint64_t dW = sdesc_sw128(sbase + kW, 16384, 1024);
+    const uint64_t dC = sdesc_sw128(sbase + kC, 16, 1024);
+    // a wait of this warp, whose every instruction delays the tensor core: tried in line
+    auto ready = [&](int b, int k) {
+      return __all_sync(~0u, mbar_try_wait(&x.bar[b], k & 1)) || x.wait(b, k);
+    };
+    // byte offset of K step k in a [128 x 128] tile, K along its rows
+    auto koff = [](int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32); };
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      const uint64_t dC = sdesc_sw128(sbase + kC + st * 32768, 16, 1024);
       const uint64_t dB = sdesc_sw128(sbase + kB + st * 32768, 16, 1024);
       const uint64_t dBt = sdesc_sw128(sbase + kB + st * 32768, 16384, 1024);
       const uint64_t dX = sdesc_sw128(sbase + kX + st * 16384, 16, 1024);
-      auto koff = [](int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32); };
-      if (!x.wait2(F_CB, i)) break;
+      if (!ready(F_BX + st, i >> 1)) break;
       if (kOut) {
-        // (G was read before W of the chunk before was ready)
+        // (the G before was read before its W was ready)
+        if (!ready(F_C, i)) break;
         tc_fence_after();
-        for (int k = 0; k < nk; ++k) mma_bf16_warp(tb + tG, sdesc_add(dC, koff(k)), sdesc_add(dB, koff(k)), idG, k > 0);
-        mma_commit_warp(&x.bar[G_DONE]);
-        if (i >= 2 && !x.wait2(Y_READ, i - 2)) break;
-        if (!x.wait(S_READY, i)) break;
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < NK; ++k) mma_bf16(tb + tG, sdesc_add(dC, koff(k)), sdesc_add(dB, koff(k)), idG, k > 0);
+          mma_commit(&x.bar[G_DONE]);
+        }
+        __syncwarp();
+        if (!ready(YX_READY, i)) break;
         tc_fence_after();
-        for (int k = 0; k < nk; ++k)
-          mma_bf16_warp(tb + tYx(i), sdesc_add(dC, koff(k)), sdesc_add(dS, k * 2048), idYx, k > 0);
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < NK; ++k) mma_bf16(tb + tYx, sdesc_add(dC, koff(k)), sdesc_add(dS, k * 2048), idYx, k > 0);
+          mma_commit(&x.bar[C_FREE]);
+        }
+        __syncwarp();
       }
-      if (!x.wait2(F_X, i) || !x.wait(WX_READY, i)) break;
-      if (i >= 1 && !x.wait(DS_READ, i - 1)) break;
+      if (!ready(WX_READY, i)) break;
       tc_fence_after();
-      for (int k = 0; k < 16; ++k)
-        mma_bf16_warp(tb + tDS, sdesc_add(dBt, (k & 7) * 2048), sdesc_add(dW, k * 2048), idDS, k > 0);
-      mma_commit_warp(&x.bar[DS_DONE]);
-      if (kOut) {
-        if (!x.wait(W_READY, i)) break;
-        tc_fence_after();
-        for (int k = 0; k < 8; ++k)
-          mma_bf16_ts_warp(tb + tYi(i), tb + tW + k * 8, sdesc_add(dX, k * 2048), idYx, k > 0);
-        mma_commit_warp(&x.bar[Y_DONE + st]);
+      if (elect_one()) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) mma_bf16(tb + tDS, sdesc_add(dBt, k * 2048), sdesc_add(dW, k * 2048), idDS, k > 0);
+        mma_commit(&x.bar[DS_DONE]);
+        if (!kOut) mma_commit(&x.bar[BX_FREE + st]);
       }
-      mma_commit_warp(&x.bar[CB_FREE + st]);
+      __syncwarp();
+      if (kOut) {
+        if (!ready(W_READY, i)) break;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) mma_bf16_ts(tb + tYi, tb + tW + 8 * k, sdesc_add(dX, k * 2048), idYx, k > 0);
+          mma_commit(&x.bar[Y_DONE + st]);
+          mma_commit(&x.bar[BX_FREE + st]);
+        }
+        __syncwarp();
+      }
     }
-    mma_commit_warp(&x.bar[DRAIN]);
+    if (elect_one()) mma_commit(&x.bar[DRAIN]);
+    __syncwarp();
     const uint64_t t0 = global_ns();
     while (!mbar_try_wait_sleep(&x.bar[DRAIN], 0, 1000000u))
       if (global_ns() - t0 > p.wait_ns) break;
-  } else if (warp >= 4 && warp < 8) {
+  } else if (kOut && warp >= 4 && warp < 12) {
     // ======================= scores =======================
-    if (kOut) {
-      const int b = warp - 4;  // this warp's rows are block b
-      const int t = 32 * b + lane;
-      {  // tokens behind this warp's block: zeros, once
-        uint32_t z[16];
-#pragma unroll
-        for (int j = 0; j < 16; ++j) z[j] = 0;
-        for (int c = b + 1; c < 4; ++c) tmem_st16(tl + tW + 16 * c, z);
-        tmem_st_wait();
-      }
-      for (int i = 0; i < n; ++i) {
-        if (!x.wait2(DEC, i) || !x.wait(G_DONE, i)) break;
-        if (i >= 1 && !x.wait2(Y_DONE, i - 1)) break;  // W is read
-        tc_fence_after();
-        const Decays &D = x.dec(i);
-        const float pre = D.pre[t], rowf = exp2f(pre);
-        for (int c = 0; c <= b; ++c) {
-          float v[32];
-          uint32_t w[16];
-          tmem_ld32(tl + tG + 32 * c, v);
-          tmem_ld_wait(v);
-          if (c < b) {
-            const float *col = D.col[b - c - 1] + 32 * c;
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = f4(col + j);
-              const float2 r2 = make_float2(rowf, rowf);
-              const float2 lo = __fmul2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), r2), make_float2(f.x, f.y));
-              const float2 hi = __fmul2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), r2), make_float2(f.z, f.w));
-              w[j / 2] = pack_bf16x2(lo.x, lo.y);
-              w[j / 2 + 1] = pack_bf16x2(hi.x, hi.y);
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; j += 4) {
-              const float4 f = f4(D.pre + 32 * c + j), d = f4(D.d + 32 * c + j);
-              const float e0 = j <= lane ? v[j] * (d.x * exp2f(pre - f.x)) : 0.f;
-              const float e1 = j + 1 <= lane ? v[j + 1] * (d.y * exp2f(pre - f.y)) : 0.f;
-              const float e2 = j + 2 <= lane ? v[j + 2] * (d.z * exp2f(pre - f.z)) : 0.f;
-              const float e3 = j + 3 <= lane ? v[j + 3] * (d.w * exp2f(pre - f.w)) : 0.f;
-              w[j / 2] = pack_bf16x2(e0, e1);
-              w[j / 2 + 1] = pack_bf16x2(e2, e3);
-            }
-          }
-          tmem_st16(tl + tW + 16 * c, w);
-        }
-        tmem_st_wait();
-        tc_fence_before();
-        x.arrive(W_READY);
-        x.arrive(DEC_FREE + (i & 1));
-      }
+    const int b = warp & 3, half = (warp - 4) >> 2;  // this warp's rows are block b, its columns a half of each block
+    const uint32_t tg = tl + tG + 16 * half, tw = tl + tW + 8 * half;
+    {  // tokens behind this warp's block: zeros, once
+      const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll 1
+      for (int c = b + 1; c < 4; ++c) tmem_st8(tw + 16 * c, z);
+      tmem_st_wait();
     }
-  } else if (warp >= 8 && warp < 12) {
-    // ======================= tokens =======================
-    const int t = 32 * (warp - 8) + lane;
-    const float skip = kOut && a.D ? a.D[h] : 0.f;
-    const float2 skip2 = make_float2(skip, skip);
-    auto output = [&](int i) {  // y of chunk i, row t
-      if (!x.wait2(Y_DONE, i)) return false;
-      tc_fence_after();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      if (!x.wait4(DEC, i)) break;
       const Decays &D = x.dec(i);
-      const float f = D.before[t >> 5] * exp2f(D.pre[t]);
-      const float2 f2 = make_float2(f, f);
-      unsigned char *xt = sm + kX + (i & 1) * 16384;
-      const int count = ch.count(i);
-      __nv_bfloat16 *yrow = (__nv_bfloat16 *)a.y + (int64_t)(row_of_seq + ch.first(i) + t) * a.y_stride + h * a.P + p0;
+      const float pre = D.pre[t], rowf = ex2(pre);
+      const float2 r2 = make_float2(rowf, rowf);
+      if (!x.wait(G_DONE, i)) break;
+      if (i >= 1 && !x.wait2(Y_DONE, i - 1)) break;  // W is read
+      tc_fence_after();
+      float v[16];
+      uint32_t w[8];
+      tmem_ld16(tg, v);
+#pragma unroll 1
+      for (int c = 0; c < b; ++c) {
+        const float *col = D.col[b - c - 1] + 32 * c + 16 * half;
+        tmem_ld_wait(v);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float yi[32], yx[32];
-        tmem_ld32(tl + tYi(i) + 32 * c, yi);
-        tmem_ld32(tl + tYx(i) + 32 * c, yx);
-        tmem_ld_wait(yi);
-        tmem_ld_touch(yx);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          uint4 *at = reinterpret_cast<uint4 *>(xt + sw128_chunk(t, 4 * c + k));
-          uint4 v = *at;
-          uint32_t *u = &v.x;
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int e = 8 * k + 2 * j;
-            const float2 xv = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j]));
-            const float2 s = __ffma2_rn(f2, make_float2(yx[e], yx[e + 1]), make_float2(yi[e], yi[e + 1]));
-            const float2 o = __ffma2_rn(skip2, xv, s);
-            u[j] = pack_bf16x2(o.x, o.y);
-          }
-          *at = v;
-          const int col = 32 * c + 8 * k;
-          if (count < Q && t < count && p0 + col < a.P) *reinterpret_cast<uint4 *>(yrow + col) = v;
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = f4(col + j);
+          const float2 lo = __fmul2_rn(make_float2(v[j], v[j + 1]), __fmul2_rn(r2, make_float2(f.x, f.y)));
+          const float2 hi = __fmul2_rn(make_float2(v[j + 2], v[j + 3]), __fmul2_rn(r2, make_float2(f.z, f.w)));
+          w[j / 2] = pack_bf16x2(lo.x, lo.y);
+          w[j / 2 + 1] = pack_bf16x2(hi.x, hi.y);
         }
+        tmem_ld16(tg + 32 * (c + 1), v);
+        tmem_st8(tw + 16 * c, w);
       }
+      float e[16];  // the diagonal block's factors, formed while its scores arrive
+#pragma unroll
+      for (int j = 0; j < 16; j += 4) {
+        const float4 f = f4(D.pre + 32 * b + 16 * half + j), d = f4(D.d + 32 * b + 16 * half + j);
+        e[j] = d.x * ex2(pre - f.x);
+        e[j + 1] = d.y * ex2(pre - f.y);
+        e[j + 2] = d.z * ex2(pre - f.z);
+        e[j + 3] = d.w * ex2(pre - f.w);
+      }
+      tmem_ld_wait(v);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2)
+        w[j / 2] = pack_bf16x2(16 * half + j <= lane ? v[j] * e[j] : 0.f, 16 * half + j + 1 <= lane ? v[j + 1] * e[j + 1] : 0.f);
+      tmem_st8(tw + 16 * b, w);
+      tmem_st_wait();
       tc_fence_before();
-      x.arrive(Y_READ + (i & 1));
-      fence_proxy_async_smem();
-      x.arrive(X_FREE + (i & 1));
-      x.arrive(DEC_FREE + (i & 1));
-      return true;
-    };
-    int i = 0;
-    for (; i < n; ++i) {
-      if (!x.wait2(DEC, i) || !x.wait2(F_X, i)) break;
-      if (i >= 1 && !x.wait(DS_DONE, i - 1)) break;  // wx is read
-      const int count = ch.count(i);
-      const bool live = t < count;
-      const float f = x.dec(i).w[t];
-      const float2 f2 = make_float2(f, f);
-      unsigned char *xt = sm + kX + (i & 1) * 16384;
+      x.arrive(W_READY);
+      x.arrive(DEC_FREE + (i & 3));
+    }
+  } else if (warp < 4) {
+    // ======================= decays (warps 1 and 3) =======================
+    const int b0 = warp & 2;  // this warp's blocks: b0, b0 + 1
+    const float A2 = a.A[h] * 1.4426950408889634f;
+    const __nv_bfloat16 *dt = (const __nv_bfloat16 *)a.dt + h;
+    const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
+    float raw[2], total = 0.f;
+    auto fetch = [&](int i) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t at = sw128_chunk(t, k);
-        const uint4 v = *reinterpret_cast<const uint4 *>(xt + at);
-        const uint32_t *u = &v.x;
-        uint4 hi, lo;
-        uint32_t *ph = &hi.x, *pl = &lo.x;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          ph[j] = split(__fmul2_rn(f2, __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u[j]))), pl[j]);
-        if (!live) hi = lo = make_uint4(0, 0, 0, 0);
-        *reinterpret_cast<uint4 *>(sm + kW + at) = hi;
-        *reinterpret_cast<uint4 *>(sm + kW + 16384 + at) = lo;
+      for (int k = 0; k < 2; ++k) {
+        const int tk = 32 * (b0 + k) + lane;
+        raw[k] = i < n && tk < ch.count(i) ? __bfloat162float(dt[(int64_t)(row_of_seq + ch.first(i) + tk) * a.dt_stride]) : 0.f;
       }
-      if (count < Q) {  // rows behind the last token: x and B sum over tokens, so they must be zeros
-        if (!x.wait2(F_CB, i)) break;
-        if (!live) {
-          const uint4 z = make_uint4(0, 0, 0, 0);
+    };
+    fetch(0);
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      float d[2], up[2], s[2];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const uint32_t at = sw128_chunk(t, k);
-            if (kOut) *reinterpret_cast<uint4 *>(xt + at) = z;
-            *reinterpret_cast<uint4 *>(sm + kB + (i & 1) * 32768 + at) = z;
-            *reinterpret_cast<uint4 *>(sm + kB + (i & 1) * 32768 + 16384 + at) = z;
+      for (int k = 0; k < 2; ++k) {
+        d[k] = raw[k] + bias;
+        if (a.softplus) d[k] = softplus_fast(d[k]);
+        if (32 * (b0 + k) + lane >= ch.count(i)) d[k] = 0.f;
+        up[k] = s[k] = d[k] * A2;
+      }
+      fetch(i + 1);
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float u = __shfl_up_sync(~0u, up[k], o), v = __shfl_down_sync(~0u, s[k], o);
+          if (lane >= o) up[k] += u;
+          if (lane + o < 32) s[k] += v;
+        }
+      }
+      if (i >= 4 && !x.wait4(DEC_FREE, i - 4)) break;
+      Decays &D = x.dec(i);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const float after = __shfl_down_sync(~0u, s[k], 1);
+        s[k] = lane < 31 ? after : 0.f;  // behind the token, to its block's end
+        if (lane == 31) D.total[b0 + k] = up[k];
+        D.d[32 * (b0 + k) + lane] = d[k];
+        D.pre[32 * (b0 + k) + lane] = up[k];
+      }
+      x.arrive(TOTALS);
+      if (!x.wait(TOTALS, i)) break;
+      const float4 L = f4(D.total);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int tk = 32 * (b0 + k) + lane;
+        float sum = s[k];
+#pragma unroll
+        for (int j = 1; j < 4; ++j) {  // block b0 + k + j
+          if (b0 + k + j < 4) {
+            if (kOut) D.col[j - 1][tk] = d[k] * ex2(sum);
+            const int nb = k + j;  // counted from b0
+            sum += nb == 1 ? (b0 ? L.w : L.y) : nb == 2 ? L.z : L.w;
           }
         }
+        D.w[tk] = d[k] * ex2(sum);
+      }
+      if (b0 == 0 && lane == 0) {
+        D.before[0] = 1.f;
+        D.before[1] = ex2(L.x);
+        D.before[2] = ex2(L.x + L.y);
+        D.before[3] = ex2(L.x + L.y + L.z);
+        D.all = ex2(L.x + L.y + L.z + L.w);
+      }
+      total += L.x + L.y + L.z + L.w;
+      x.arrive(DEC + (i & 3));
+    }
+    if (!kOut && b0 == 0 && lane == 0 && p0 == 0) p.decays[it.item * a.H + h] = ex2(total);
+  } else if (warp >= 12 && warp < 16) {
+    // ======================= tokens =======================
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const bool live = t < ch.count(i);
+      if (!x.wait4(DEC, i)) break;
+      const float w = x.dec(i).w[t];
+      x.arrive(DEC_FREE + (i & 3));
+      const float2 f2 = make_float2(w, w);
+      if (!x.wait2(F_BX, i)) break;
+      unsigned char *xt = sm + kX + (i & 1) * 16384;
+      auto load = [&](int k) {
+        return live ? *reinterpret_cast<const uint4 *>(xt + sw128_chunk(t, k)) : make_uint4(0, 0, 0, 0);
+      };
+      uint4 v = load(0);
+      if (!live) {  // rows behind the last token: x and B sum over tokens, so they must be zeros
+        const uint4 z = make_uint4(0, 0, 0, 0);
+        unsigned char *bt = sm + kB + (i & 1) * 32768;
+#pragma unroll 1
+        for (int k = 0; k < 8; ++k) {
+          const uint32_t at = sw128_chunk(t, k);
+          if (kOut) *reinterpret_cast<uint4 *>(xt + at) = z;
+          *reinterpret_cast<uint4 *>(bt + at) = z;
+          *reinterpret_cast<uint4 *>(bt + 16384 + at) = z;
+        }
+      }
+      if (i >= 1 && !x.wait(DS_DONE, i - 1)) break;  // wx is read
+#pragma unroll 2
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+        v = load((k + 1) & 7);
+        uint32_t q0[4], q1[4], q2[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 y = __fmul2_rn(f2, unpack(u[j]));
+          q0[j] = take_term(y);
+          q1[j] = take_term(y);
+          q2[j] = pack_bf16x2(y.x, y.y);
+        }
+        unsigned char *to = sm + kW + sw128_chunk(t, k);
+        *reinterpret_cast<uint4 *>(to) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
+        *reinterpret_cast<uint4 *>(to + 16384) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
+        *reinterpret_cast<uint4 *>(to + 32768) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
       }
       fence_proxy_async_smem();
       x.arrive(WX_READY);
-      if (kOut) {
-        if (i >= 1 && !output(i - 1)) break;
-      } else {
-        x.arrive(X_FREE + (i & 1));
-        x.arrive(DEC_FREE + (i & 1));
-      }
     }
-    if (kOut && i == n) output(n - 1);
-  } else if (warp >= 12) {
+  } else if (warp >= 16 && warp < 24) {
     // ======================= state =======================
-    const int row = 32 * (warp - 12) + lane;
-    const bool live = row < a.N;
-    const int cols = min(PC, a.P - p0);
-    const int64_t np = (int64_t)a.N * a.P, at = (int64_t)row * a.P + p0;
-    float S[PC];
+    const int half = (warp - 16) >> 2;
+    const int cols = t < a.N ? min(32, a.P - p0 - 32 * half) : 0;  // columns that exist
+    const int64_t np = (int64_t)a.N * a.P, at = (int64_t)t * a.P + p0 + 32 * half;
+    float S[32];
     const float *from = nullptr;
-    if (kOut && live) {
+    if (kOut) {
       if (p.seg != 0) from = p.ws + (it.item * a.H + h) * np + at;
       else if (a.state && it.s.ctx > 0) from = a.state + ((int64_t)it.s.slot * a.H + h) * np + at;
     }
 #pragma unroll
-    for (int j = 0; j < PC; j += 4) {
+    for (int j = 0; j < 32; j += 4) {
       const float4 v = from && j < cols ? f4(from + j) : make_float4(0.f, 0.f, 0.f, 0.f);
       S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
     }
-    auto save = [&](float *to) {
-      if (!live) return;
+    auto copy = [&]() {  // the bf16 copy that the next chunk's outputs read
 #pragma unroll
-      for (int j = 0; j < PC; j += 4)
-        if (j < cols) *reinterpret_cast<float4 *>(to + at + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
-    };
-    int i = 0;
-    for (; i < n; ++i) {
-      if (kOut) {  // (the products that read the copy before this one are done: DS_DONE)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          uint4 v;
-          v.x = pack_bf16x2(S[8 * k + 0], S[8 * k + 1]);
-          v.y = pack_bf16x2(S[8 * k + 2], S[8 * k + 3]);
-          v.z = pack_bf16x2(S[8 * k + 4], S[8 * k + 5]);
-          v.w = pack_bf16x2(S[8 * k + 6], S[8 * k + 7]);
-          *reinterpret_cast<uint4 *>(sm + kS + sw128_chunk(row, k)) = v;
-        }
-        fence_proxy_async_smem();
-        x.arrive(S_READY);
+      for (int k = 0; k < 4; ++k) {
+        uint4 v;
+        v.x = pack_bf16x2(S[8 * k + 0], S[8 * k + 1]);
+        v.y = pack_bf16x2(S[8 * k + 2], S[8 * k + 3]);
+        v.z = pack_bf16x2(S[8 * k + 4], S[8 * k + 5]);
+        v.w = pack_bf16x2(S[8 * k + 6], S[8 * k + 7]);
+        *reinterpret_cast<uint4 *>(sm + kS + sw128_chunk(t, 4 * half + k)) = v;
       }
-      if (!x.wait2(DEC, i)) break;
+      fence_proxy_async_smem();
+      x.arrive(YX_READY);
+    };
+    if (kOut) copy();
+    x.arrive(WX_READY);  // no dS before the first
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      if (!x.wait4(DEC, i)) break;
       const float keep = x.dec(i).all;
-      x.arrive(DEC_FREE + (i & 1));
+      x.arrive(DEC_FREE + (i & 3));
       if (!x.wait(DS_DONE, i)) break;
       tc_fence_after();
 #pragma unroll
-      for (int c = 0; c < 2; ++c) {
-        float v[32];
-        tmem_ld32(tl + tDS + 32 * c, v);
-        tmem_ld_wait(v);
+      for (int c = 0; c < 32; c += 8) {
+        float q0[8], q1[8], q2[8];
+        tmem_ld8(tl + tDS + 32 * half + c, q0);
+        tmem_ld8(tl + tDS + 64 + 32 * half + c, q1);
+        tmem_ld8(tl + tDS + 128 + 32 * half + c, q2);
+        tmem_ld_wait(q0);
+        tmem_ld_touch(q1);
+        tmem_ld_touch(q2);
 #pragma unroll
-        for (int j = 0; j < 32; ++j) S[32 * c + j] = fmaf(keep, S[32 * c + j], v[j]);
+        for (int j = 0; j < 8; ++j) S[c + j] = fmaf(keep, S[c + j], q0[j] + (q1[j] + q2[j]));
       }
       tc_fence_before();
-      x.arrive(DS_READ);
-      if (kOut && a.page) {
-        const int64_t pos = (int64_t)it.s.ctx + ch.first(i) + ch.count(i);
-        if (float *to = snapshot(a, it.r, h, pos, p0 == 0 && row == 0)) save(to);
+      x.arrive(WX_READY);
+      if (kOut && i + 1 < n) copy();  // (DS_DONE: the products that read the copy before are done)
+      // after the chunk: a snapshot, and after the last one the state's own place
+      float *to = nullptr, *last = nullptr;
+      if (kOut && a.page) to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(ch.first(i) + ch.count(i)), p0 == 0 && t == 0);
+      if (i == n - 1) {
+        if (!kOut) last = p.ws + (it.item * a.H + h) * np;
+        else if (a.state && it.index == it.count - 1) last = a.state + ((int64_t)it.s.slot * a.H + h) * np;
+      }
+#pragma unroll 1
+      for (int k = 0; k < 2; ++k, to = last) {
+        if (!to) continue;
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          if (j < cols) *reinterpret_cast<float4 *>(to + at + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
       }
     }
-    if (i == n) {
-      if (!kOut) save(p.ws + (it.item * a.H + h) * np);
-      else if (a.state && it.index == it.count - 1) save(a.state + ((int64_t)it.s.slot * a.H + h) * np);
+  } else if (kOut && warp >= 24) {
+    // ======================= outputs =======================
+    const int half = (warp - 24) >> 2;
+    const int col0 = p0 + 32 * half;
+    const float skip = a.D ? a.D[h] : 0.f;
+    const float2 skip2 = make_float2(skip, skip);
+    unsigned char *ytile = sm + kY + (warp - 24) * 2048;  // this warp's 32 rows of 32 columns (64-byte swizzle)
+    x.arrive(YX_READY);  // no Yi and Yx before the first
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int count = ch.count(i), first = row_of_seq + ch.first(i);
+      if (!x.wait4(DEC, i)) break;
+      const float f = x.dec(i).before[warp & 3] * ex2(x.dec(i).pre[t]);
+      x.arrive(DEC_FREE + (i & 3));
+      const float2 f2 = make_float2(f, f);
+      bulk_wait_read_all();  // (the lane that issued the store before)
+      __syncwarp();
+      if (!x.wait2(F_BX, i) || !x.wait2(Y_DONE, i)) break;
+      tc_fence_after();
+      const unsigned char *xt = sm + kX + (i & 1) * 16384;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float yi[16], yx[16];
+        tmem_ld16(tl + tYi + 32 * half + 16 * c, yi);
+        tmem_ld16(tl + tYx + 32 * half + 16 * c, yx);
+        tmem_ld_wait(yi);
+        tmem_ld_touch(yx);
+        if (c == 1) {
+          tc_fence_before();
+          x.arrive(YX_READY);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const uint4 v = *reinterpret_cast<const uint4 *>(xt + sw128_chunk(t, 4 * half + 2 * c + k));
+          const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+          uint32_t o[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int e = 8 * k + 2 * j;
+            const float2 s = __ffma2_rn(f2, make_float2(yx[e], yx[e + 1]), make_float2(yi[e], yi[e + 1]));
+            const float2 r = __ffma2_rn(skip2, unpack(u[j]), s);
+            o[j] = pack_bf16x2(r.x, r.y);
+          }
+          *reinterpret_cast<uint4 *>(ytile + sw64_chunk(lane, 2 * c + k)) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+      }
+      x.arrive(BX_FREE + (i & 1));
+      if (col0 >= a.P) continue;
+      if (count == Q) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        tma_store_3d_warp(&my, ytile, col0, h, first + 32 * (warp & 3));
+        bulk_commit_warp();
+      } else if (t < count) {  // a ragged chunk: only its rows
+        __nv_bfloat16 *yrow = (__nv_bfloat16 *)a.y + (int64_t)(first + t) * a.y_stride + h * a.P + col0;
+#pragma unroll 1
+        for (int k = 0; k < 4 && col0 + 8 * k < a.P; ++k)
+          *reinterpret_cast<uint4 *>(yrow + 8 * k) = *reinterpret_cast<const uint4 *>(ytile + sw64_chunk(lane, k));
+      }
     }
+    bulk_wait_read_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -598,13 +698,34 @@ bool ssm_tc_fits(const SsmArgs &a) {
   return a.bf16 && row16(a.x, a.x_stride) && row16(a.B, a.b_stride) && row16(a.C, a.c_stride) && row16(a.y, a.y_stride);
 }
 
+namespace {
+
+template <int NK>
+cudaError_t launch_nk(const CUtensorMap &mx, const CUtensorMap &mb, const CUtensorMap &mc, const CUtensorMap &my,
+                      const TcArgs &p, unsigned grid, cudaStream_t st) {
+  constexpr cudaFuncAttribute smem = cudaFuncAttributeMaxDynamicSharedMemorySize;
+  cudaError_t e = cudaFuncSetAttribute(ssm_tc_kernel<true, NK>, smem, kSmemBytes);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(ssm_tc_kernel<false, NK>, smem, kSmemBytes);
+  if (e != cudaSuccess) return e;
+  if (p.seg) {
+    ssm_tc_kernel<false, NK><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) e = launch_segment_states(p.a, p.seg, st);
+    if (e != cudaSuccess) return e;
+  }
+  ssm_tc_kernel<true, NK><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
 cudaError_t launch_ssm_tc(const SsmArgs &a, int seg, cudaStream_t st) {
   CUtensorMap mx, mb, mc, my;
   const uint64_t rows = (uint64_t)a.q.rows;
   if (!encode_tmap_bf16_rows(&mx, a.x, a.P, a.H, rows, a.x_stride, PC, Q) ||
       !encode_tmap_bf16_rows(&mb, a.B, a.N, a.G, rows, a.b_stride, 64, Q) ||
       !encode_tmap_bf16_rows(&mc, a.C, a.N, a.G, rows, a.c_stride, 64, Q) ||
-      !encode_tmap_bf16_rows(&my, a.y, a.P, a.H, rows, a.y_stride, PC, Q))
+      !encode_tmap_bf16_rows(&my, a.y, a.P, a.H, rows, a.y_stride, 32, 32))
     return cudaErrorInvalidValue;
   const int64_t items = scan_items(a.q.R, a.q.rows, seg);
   TcArgs p;
@@ -614,18 +735,12 @@ cudaError_t launch_ssm_tc(const SsmArgs &a, int seg, cudaStream_t st) {
   p.decays = seg ? seg_decays(a, items) : nullptr;
   p.wait_ns = debug_wait_ns();
   const unsigned grid = (unsigned)(items * a.H * ((a.P + PC - 1) / PC));
-  cudaError_t e = cudaFuncSetAttribute(ssm_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(ssm_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-  if (e != cudaSuccess) return e;
-  if (seg) {
-    ssm_tc_kernel<false><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_segment_states(a, seg, st);
-    if (e != cudaSuccess) return e;
+  switch (a.N) {
+    case 16: return launch_nk<1>(mx, mb, mc, my, p, grid, st);
+    case 32: return launch_nk<2>(mx, mb, mc, my, p, grid, st);
+    case 64: return launch_nk<4>(mx, mb, mc, my, p, grid, st);
+    default: return launch_nk<8>(mx, mb, mc, my, p, grid, st);
   }
-  ssm_tc_kernel<true><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);
-  return cudaGetLastError();
 }
 
 }  // namespace kda
