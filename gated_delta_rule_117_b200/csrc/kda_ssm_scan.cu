@@ -17,6 +17,8 @@
 // the token loop has no barrier: a token costs 3 N / 4 operations a thread and
 // two shuffles.  Tokens are staged in shared memory TB at a time.  Its chain of
 // dependent tokens bounds it, not bytes.
+#include <math.h>
+
 #include "kda_ssm_seg.cuh"
 
 namespace kda {
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
 
 // Entering states of every segment of a sequence, in place of what the segments
 // add to a zero state: S(0) from the pool, S(i + 1) = a_i S(i) + S~_i.
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 128, kAhead = 8;
 __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a, int seg, float4 *ws,
                                                                       const float *decays) {
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H;
@@ -135,30 +137,66 @@ __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a,
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.state && s.ctx > 0)
     S = reinterpret_cast<const float4 *>(a.state)[((int64_t)s.slot * a.H + h) * n4 + e];
-  for (int i = 0; i < count; ++i) {
-    float4 *w = ws + ((base + i) * a.H + h) * n4 + e;
-    float4 add = make_float4(0.f, 0.f, 0.f, 0.f);
-    float keep = 0.f;
-    if (i + 1 < count) {
-      add = *w;
-      keep = decays[(base + i) * a.H + h];
+  float4 *w = ws + (base * a.H + h) * n4 + e;
+  const float *dec = decays + base * a.H + h;
+  const int64_t step = (int64_t)a.H * n4;
+  // kAhead segments' loads in flight together: only the sums depend on one another
+  // (16 heads of 128 x 128, 10 segments: 37 us one by one)
+  for (int i0 = 0; i0 < count; i0 += kAhead) {
+    float4 add[kAhead];
+    float keep[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      const bool some = i0 + k + 1 < count;  // (the last segment's is neither computed nor needed)
+      add[k] = some ? w[(i0 + k) * step] : make_float4(0.f, 0.f, 0.f, 0.f);
+      keep[k] = some ? dec[(int64_t)(i0 + k) * a.H] : 0.f;
     }
-    *w = S;
-    S.x = fmaf(keep, S.x, add.x);
-    S.y = fmaf(keep, S.y, add.y);
-    S.z = fmaf(keep, S.z, add.z);
-    S.w = fmaf(keep, S.w, add.w);
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) {
+      if (i0 + k < count) w[(i0 + k) * step] = S;
+      S.x = fmaf(keep[k], S.x, add[k].x);
+      S.y = fmaf(keep[k], S.y, add[k].y);
+      S.z = fmaf(keep[k], S.z, add[k].z);
+      S.w = fmaf(keep[k], S.w, add[k].w);
+    }
   }
 }
 
-// Segment length of the CUDA-core kernel: none while the sequences' heads give
-// every SM a block (or prompts are short), else as many as do.
-int simt_segment(int R, int rows, int H) {
-  const int64_t chains = (int64_t)R * H;
-  if (chains >= 148 || rows < 2 * kAlign) return 0;
-  const int64_t want = (148 + H - 1) / H;  // segments in all
-  const int64_t seg = ((rows + want - 1) / want + kAlign - 1) / kAlign * kAlign;
-  return (int)seg;
+// Segment length (a multiple of kAlign), or 0 for whole sequences: the choice whose
+// blocks' waves over the SMs cost least.
+//   blocks : blocks that an item of `H` heads makes
+//   resident : blocks that run at once
+//   state_cost : time of a state pass over a chunk, in output passes
+//   launch_cost : time of the two more launches, in tokens of the output pass
+// Whole sequences run as long as the longest of them; packed ones (whose lengths
+// the host does not see) are taken to hold one of twice the mean.
+int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int launch_cost, bool packed) {
+  auto waves = [&](double items) { return ceil(items * blocks / resident); };
+  const double mean = (double)rows / R;
+  const double most = packed && R > 1 ? fmin((double)rows, 2 * mean) : mean;
+  // blocks of unequal length fill the machine as they come: the waves' total, or the longest block
+  double best = packed && R > 1 ? fmax(most, mean * R * blocks / resident) : waves(R) * mean;
+  int seg = 0;
+  for (int k = 2; k <= 64; ++k) {
+    const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
+    if (len < 4 * kAlign) break;
+    const double items = packed && R > 1 ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
+    const double cost = waves(items) * len * (1 + state_cost) + launch_cost;
+    if (cost < best) {
+      best = cost;
+      seg = len;
+    }
+  }
+  return seg;
+}
+
+// The CUDA-core kernel: two blocks of 512 threads share an SM; a token takes about
+// 0.2 us, its state pass saves the outputs' half.
+int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 64, packed); }
+// The tensor-core kernel: one block an SM; a chunk takes 2.6 us, 1.1 us in the state
+// pass; the two launches about 10 us.
+int tc_segment(int R, int rows, int H, int P, bool packed) {
+  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.43f, 4 * kAlign, packed);
 }
 
 template <int N, int P, typename T>
@@ -185,14 +223,23 @@ cudaError_t launch_segment_states(const SsmArgs &a, int seg, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+// Enough for every form that a call of these sizes may take (packed or not, rows that
+// fit the tensor-core kernel or not).
 size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16) {
-  const int seg = simt_segment(R, rows, H);
-  return seg ? seg_workspace(scan_items(R, rows, seg), H, N, P) : 0;
+  size_t most = 0;
+  for (int packed = 0; packed < 2; ++packed)
+    for (int tc = 0; tc <= (bf16 ? 1 : 0); ++tc) {
+      const int seg = tc ? tc_segment(R, rows, H, P, packed) : simt_segment(R, rows, H, packed);
+      const size_t need = seg ? seg_workspace(scan_items(R, rows, seg), H, N, P) : 0;
+      most = need > most ? need : most;
+    }
+  return most;
 }
 
 cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st) {
-  const int seg = simt_segment(a.q.R, a.q.rows, a.H);
-  if (ssm_tc_fits(a)) return launch_ssm_tc(a, seg, st);
+  const bool packed = a.q.cu != nullptr;
+  if (ssm_tc_fits(a)) return launch_ssm_tc(a, tc_segment(a.q.R, a.q.rows, a.H, a.P, packed), st);
+  const int seg = simt_segment(a.q.R, a.q.rows, a.H, packed);
 #define KDA_SSM_CASE(NN, PP)    \
   if (a.N == NN && a.P == PP)   \
     return a.bf16 ? launch_t<NN, PP, __nv_bfloat16>(a, seg, st) : launch_t<NN, PP, float>(a, seg, st);
