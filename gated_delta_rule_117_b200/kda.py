@@ -473,83 +473,118 @@ def spec_replay_verify_fused(q, k, v, z, A_log, beta, S, gate, rms_weight, n_rep
 # to be dense.  Integer arguments (cu, ctx, slots, lengths, tables) are int32
 # tensors on the same device and are not read on the host.
 
-def _on(device, *tensors):
+# The checks below run on every call of a few microseconds, so each helper tests
+# what a right call has in one expression of attribute reads, and only then, to
+# name what is wrong, goes through the checks that raise.
+
+def _on(x, *tensors):
+    """Every tensor on x's CUDA device."""
+    d = x.get_device()
+    if d < 0:
+        raise ValueError("libkda takes CUDA tensors")
     for t in tensors:
-        if t is not None and t.device != device:
-            raise ValueError("all tensors of a call must be on one CUDA device (got %s and %s)" % (device, t.device))
+        if t is not None and t.get_device() != d:
+            raise ValueError("all tensors of a call must be on one CUDA device (got %s and %s)" % (x.device, t.device))
 
 
-def _typed(dtype, **tensors):
-    import torch
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
+def _typed(dtype, names, *tensors):
+    for name, t in zip(names.split(), tensors):
+        if t is not None and t.dtype is not dtype:
             raise TypeError("%s must be %s, got %s" % (name, str(dtype).replace("torch.", ""), t.dtype))
 
 
 def _shaped(name, t, shape):
-    if t is not None and tuple(t.shape) != tuple(shape):
+    if t is not None and t.shape != shape:
         raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
 
 
-def _rows(name, t, lead, cuda=True):
+def _dense(names, *tensors):
+    for name, t in zip(names.split(), tensors):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("%s must be contiguous" % name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(name, t, lead):
     """Row stride of token-major `t`: `lead` leading dimensions of rows over dense rows of elements."""
-    if cuda and not t.is_cuda:
-        raise ValueError("libkda takes CUDA tensors")
+    if lead == 1 and t.is_contiguous():
+        return t.stride(0) if t.size(0) > 1 else t.numel()
     shape, stride = t.shape, t.stride()
     want = 1
-    for i in range(t.dim() - 1, lead - 1, -1):
+    for i in range(len(shape) - 1, lead - 1, -1):
         if shape[i] != 1 and stride[i] != want:
             raise ValueError("%s: the elements of a row must be dense" % name)
         want *= shape[i]
-    if lead == 2 and shape[0] > 1 and shape[1] > 1 and stride[0] != shape[1] * stride[1]:
+    if lead == 1:
+        return stride[0] if shape[0] > 1 else want
+    n0, n1 = shape[0], shape[1]
+    if n0 > 1 and n1 > 1 and stride[0] != n1 * stride[1]:
         raise ValueError("%s: rows must have one stride" % name)
-    rows = shape[0] if lead == 1 else shape[0] * shape[1]
-    if rows <= 1:
-        return want
-    return stride[lead - 1] if shape[lead - 1] > 1 else stride[0]
+    return want if n0 * n1 <= 1 else stride[1] if n1 > 1 else stride[0]
 
 
-class _Call:
-    """The device's stream for a call, with that device current."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.other = None if device.index is None or device.index == torch.cuda.current_device() else torch.cuda.device(device)
-        self.stream, self.device = stream, device
-
-    def __enter__(self):
-        import torch
-        if self.other is not None:
-            self.other.__enter__()
-        if self.stream is None:
-            return torch.cuda.current_stream(self.device).cuda_stream
-        return getattr(self.stream, "cuda_stream", self.stream)
-
-    def __exit__(self, *exc):
-        if self.other is not None:
-            self.other.__exit__(*exc)
+_torch = _device = _raw_stream = None
 
 
-def _check(code, what):
+def _init():
+    global _torch, _device, _raw_stream
+    import torch
+    _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda i: torch.cuda.current_stream(i).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _launch(fn, what, i, stream, args):
+    """Call `fn` of the library on the stream (its last argument; None: the current one) with device i current."""
+    stream = _raw_stream(i) if stream is None else getattr(stream, "cuda_stream", stream)
+    if i == _device():
+        code = fn(*args, stream)
+    else:
+        with _torch.cuda.device(i):
+            code = fn(*args, stream)
     if code != KDA_OK:
         raise KdaError(code, what)
 
 
-def _requests(x, lead, state, slots, ctx, cu):
+def _good_slots(t, R, d, i32):
+    """Whether t is a vector of R int32 on device d (or None)."""
+    return t is None or (t.dtype is i32 and t.dim() == 1 and t.size(0) == R and t.get_device() == d and t.is_contiguous())
+
+
+def _good_vector(t, n, d, dtype):
+    """The same for a parameter vector."""
+    return t is None or (t.dtype is dtype and t.dim() == 1 and t.size(0) == n and t.get_device() == d and t.is_contiguous())
+
+
+def _bad_requests(slots, ctx, cu, R):
+    i32 = _torch.int32
+    _typed(i32, "slots ctx cu", slots, ctx, cu)
+    _dense("slots ctx cu", slots, ctx, cu)
+    _shaped("slots", slots, (R,))
+    _shaped("ctx", ctx, (R,))
+    raise ValueError("slots and ctx must be [R], cu [R + 1] int32 on the device of the call")
+
+
+def _requests(x, lead, slots, ctx, cu, d):
     """(R, rows) of a packed call, after the checks of its integer arguments."""
-    import torch
-    _typed(torch.int32, slots=slots, ctx=ctx, cu=cu)
+    i32 = _torch.int32
     if lead == 2:
         if cu is not None:
             raise ValueError("cu goes with [rows, ...] tensors")
-        R, rows = x.shape[0], x.shape[0] * x.shape[1]
+        R = x.size(0)
+        rows = R * x.size(1)
     else:
-        rows = x.shape[0]
+        rows = x.size(0)
         R = 1 if cu is None else cu.numel() - 1
         if R < 0:
             raise ValueError("cu must hold R + 1 offsets")
-    _shaped("slots", slots, (R,))
-    _shaped("ctx", ctx, (R,))
+    if not (_good_slots(slots, R, d, i32) and _good_slots(ctx, R, d, i32) and _good_slots(cu, R + 1, d, i32)):
+        _on(x, slots, ctx, cu)
+        _bad_requests(slots, ctx, cu, R)
     return R, rows
 
 
@@ -560,39 +595,59 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
     int32; block_table: [R, blocks] int32, updated in place; rows: the most new
     tokens that the call may hold.  Returns (cu [R + 1] int32, token_slots [rows]
     int64, pages_used [1] int32)."""
-    import torch
-    _typed(torch.int32, lens=lens, ctx=ctx, free_pages=free_pages, block_table=block_table, cu=cu, pages_used=pages_used)
-    _typed(torch.int64, token_slots=token_slots)
-    dev, R = lens.device, lens.numel()
-    _on(dev, ctx, free_pages, block_table, cu, token_slots, pages_used)
-    _shaped("ctx", ctx, (R,))
-    if block_table.dim() != 2 or block_table.shape[0] != R:
-        raise ValueError("block_table must be [R, blocks]")
+    torch = _torch or _init()
+    i32, R, d = torch.int32, lens.numel(), lens.get_device()
+    if not (d >= 0 and _good_slots(lens, R, d, i32) and _good_slots(ctx, R, d, i32) and
+            _good_slots(free_pages, free_pages.numel(), d, i32) and block_table.dtype is i32 and block_table.dim() == 2 and
+            block_table.size(0) == R and block_table.get_device() == d and block_table.is_contiguous()):
+        _typed(i32, "lens ctx free_pages block_table", lens, ctx, free_pages, block_table)
+        _dense("lens ctx free_pages block_table", lens, ctx, free_pages, block_table)
+        _on(lens, ctx, free_pages, block_table)
+        _shaped("ctx", ctx, (R,))
+        raise ValueError("lens and ctx must be [R], free_pages [n], block_table [R, blocks]")
+    given = cu is not None or token_slots is not None or pages_used is not None
     if cu is None:
-        cu = torch.empty(R + 1, dtype=torch.int32, device=dev)
+        cu = lens.new_empty(R + 1)
     if token_slots is None:
-        token_slots = torch.empty(rows, dtype=torch.int64, device=dev)
+        token_slots = lens.new_empty(rows, dtype=torch.int64)
     if pages_used is None:
-        pages_used = torch.empty(1, dtype=torch.int32, device=dev)
-    _shaped("cu", cu, (R + 1,))
-    _shaped("token_slots", token_slots, (rows,))
-    _shaped("pages_used", pages_used, (1,))
-    with _Call(dev, stream) as st:
-        _check(kda_block_map(_ptr(lens), _ptr(ctx), _ptr(free_pages), free_pages.numel(), _ptr(block_table),
-                             block_table.shape[1], page_size, _ptr(cu), _ptr(token_slots), _ptr(pages_used), R, rows, st),
-               "kda_block_map")
+        pages_used = lens.new_empty(1)
+    if given:
+        _shaped("cu", cu, (R + 1,))
+        _shaped("token_slots", token_slots, (rows,))
+        _shaped("pages_used", pages_used, (1,))
+        _typed(i32, "cu pages_used", cu, pages_used)
+        _typed(torch.int64, "token_slots", token_slots)
+        _dense("cu token_slots pages_used", cu, token_slots, pages_used)
+        _on(lens, cu, token_slots, pages_used)
+    _launch(load_library().kda_block_map, "kda_block_map", d, stream,
+            (lens.data_ptr(), _at(ctx), free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
+             block_table.size(1), page_size, cu.data_ptr(), token_slots.data_ptr(), pages_used.data_ptr(), R, rows))
     return cu, token_slots, pages_used
 
 
-def _conv_weights(x, w, bias, state, C):
-    _typed(x.dtype, w=w, bias=bias, state=state)
-    _on(x.device, w, bias, state)
-    if w.dim() != 2 or w.shape[0] != C:
-        raise ValueError("w must be [C, K]")
-    K = w.shape[1]
-    _shaped("bias", bias, (C,))
-    if state is not None:
-        _shaped("state", state, (state.shape[0], K - 1, C))
+def _output(x, y, lead, width):
+    """(y, its row stride) for a token-major output like x."""
+    if y is None:
+        return _torch.empty_like(x, memory_format=_torch.contiguous_format), width
+    _typed(x.dtype, "y", y)
+    _shaped("y", y, x.shape)
+    _on(x, y)
+    return y, _rows("y", y, lead)
+
+
+def _conv_weights(x, w, bias, state, C, d):
+    """The number of taps, after the checks of weights and pool."""
+    t = x.dtype
+    K = w.size(1) if w.dim() == 2 else 0
+    if not (d >= 0 and K > 0 and w.dtype is t and w.size(0) == C and w.get_device() == d and w.is_contiguous() and
+            _good_vector(bias, C, d, t) and
+            (state is None or (state.dtype is t and state.dim() == 3 and state.size(1) == K - 1 and state.size(2) == C and
+                               state.get_device() == d and state.is_contiguous()))):
+        _typed(t, "w bias state", w, bias, state)
+        _dense("w bias state", w, bias, state)
+        _on(x, w, bias, state)
+        raise ValueError("w must be [C, K], bias [C], state [n_slots, K - 1, C]")
     return K
 
 
@@ -603,35 +658,31 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
     sequence), or [B, T, C]; w: [C, K]; bias: [C]; state: pool [n_slots, K - 1, C],
     updated in place; slots, ctx: [R] int32.  Returns y like x, or with
     head_major [B, C // head_dim, T, head_dim], which chunk_fwd reads."""
-    import torch
+    torch = _torch or _init()
+    code = _dtype_code(x)
     lead = x.dim() - 1
     if lead not in (1, 2):
         raise ValueError("x must be [rows, C] or [B, T, C]")
-    C = x.shape[-1]
-    R, rows = _requests(x, lead, state, slots, ctx, cu)
-    K = _conv_weights(x, w, bias, state, C)
-    _on(x.device, slots, ctx, cu, y)
-    xs = _rows("x", x, lead)
-    if head_major:
+    C, d = x.size(lead), x.get_device()
+    K = _conv_weights(x, w, bias, state, C, d)
+    R, rows = _requests(x, lead, slots, ctx, cu, d)
+    if not head_major:
+        y, ys = _output(x, y, lead, C)
+    else:
         if head_dim <= 0 or C % head_dim:
             raise ValueError("head_major needs a head_dim that divides C")
-        shape = (R, C // head_dim, rows // max(R, 1), head_dim)
-    else:
-        shape = x.shape
-    if y is None:
-        y = torch.empty(shape, dtype=x.dtype, device=x.device)
-    _typed(x.dtype, y=y)
-    _shaped("y", y, shape)
-    if head_major:
-        _ptr(y)  # dense
-        ys = C
-    else:
-        ys = _rows("y", y, lead)
+        shape, ys = (R, C // head_dim, rows // max(R, 1), head_dim), C
+        if y is None:
+            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+        else:
+            _typed(x.dtype, "y", y)
+            _shaped("y", y, shape)
+            _dense("y", y)
+            _on(x, y)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0) | (KDA_CONV_HEAD_MAJOR if head_major else 0)
-    with _Call(x.device, stream) as st:
-        _check(kda_short_conv(x.data_ptr(), xs, _ptr(w), _ptr(bias), _ptr(state), 0 if state is None else state.shape[0],
-                              _ptr(slots), _ptr(ctx), _ptr(cu), y.data_ptr(), ys, R, rows, C, K, head_dim,
-                              _dtype_code(x), flags, float(eps), st), "kda_short_conv")
+    _launch(load_library().kda_short_conv, "kda_short_conv", d, stream,
+            (x.data_ptr(), _rows("x", x, lead), w.data_ptr(), _at(bias), _at(state), 0 if state is None else state.size(0),
+             _at(slots), _at(ctx), _at(cu), y.data_ptr(), ys, R, rows, C, K, head_dim, code, flags, eps))
     return y
 
 
@@ -639,42 +690,42 @@ def short_conv_step(x, w, state, bias=None, *, slots=None, silu=True, head_dim=0
                     stream=None):
     """short_conv for one new token of each of R sequences: x [R, C]; state: pool
     [n_slots, K - 1, C], shifted in place.  Returns y [R, C]."""
-    import torch
+    torch = _torch or _init()
+    code = _dtype_code(x)
     if x.dim() != 2:
         raise ValueError("x must be [R, C]")
-    R, C = x.shape
-    K = _conv_weights(x, w, bias, state, C)
-    _typed(torch.int32, slots=slots)
-    _shaped("slots", slots, (R,))
-    _on(x.device, slots, y)
-    xs = _rows("x", x, 1)
-    if y is None:
-        y = torch.empty(R, C, dtype=x.dtype, device=x.device)
-    _typed(x.dtype, y=y)
-    _shaped("y", y, (R, C))
+    R, C, d = x.size(0), x.size(1), x.get_device()
+    K = _conv_weights(x, w, bias, state, C, d)
+    if not _good_slots(slots, R, d, torch.int32):
+        _on(x, slots)
+        _bad_requests(slots, None, None, R)
+    y, ys = _output(x, y, 1, C)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0)
-    with _Call(x.device, stream) as st:
-        _check(kda_short_conv_step(x.data_ptr(), xs, _ptr(w), _ptr(bias), _ptr(state), state.shape[0], _ptr(slots),
-                                   y.data_ptr(), _rows("y", y, 1), R, C, K, head_dim, _dtype_code(x), flags, float(eps),
-                                   st), "kda_short_conv_step")
+    _launch(load_library().kda_short_conv_step, "kda_short_conv_step", d, stream,
+            (x.data_ptr(), _rows("x", x, 1), w.data_ptr(), _at(bias), state.data_ptr(), state.size(0), _at(slots),
+             y.data_ptr(), ys, R, C, K, head_dim, code, flags, eps))
     return y
 
 
-def _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead):
-    """(H, G, N, P, row strides) after the checks of shapes, types and devices."""
-    import torch
-    H, P = x.shape[-2:]
-    G, N = B.shape[-2:]
-    _typed(x.dtype, dt=dt, B=B, C=C)
-    _typed(torch.float32, A=A, D=D, dt_bias=dt_bias, state=state)
-    _on(x.device, dt, A, B, C, D, dt_bias, state)
-    _shaped("dt", dt, x.shape[:-1])
-    _shaped("B", B, x.shape[:lead] + (G, N))
-    _shaped("C", C, B.shape)
-    for name, t in (("A", A), ("D", D), ("dt_bias", dt_bias)):
-        _shaped(name, t, (H,))
-    if state is not None:
-        _shaped("state", state, (state.shape[0], H, N, P))
+def _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d):
+    """(H, G, N, P, row strides) after the checks of shapes, types and layouts."""
+    f32, t = _torch.float32, x.dtype
+    H, P, G, N = x.size(lead), x.size(lead + 1), B.size(-2), B.size(-1)
+    shape, bshape = x.shape, B.shape
+    if not (d >= 0 and dt.dtype is t and B.dtype is t and C.dtype is t and dt.shape == shape[:-1] and
+            bshape[:-2] == shape[:-2] and C.shape == bshape and dt.get_device() == d and B.get_device() == d and
+            C.get_device() == d and _good_vector(A, H, d, f32) and _good_vector(D, H, d, f32) and
+            _good_vector(dt_bias, H, d, f32) and
+            (state is None or (state.dtype is f32 and state.dim() == 4 and state.size(1) == H and state.size(2) == N and
+                               state.size(3) == P and state.get_device() == d and state.is_contiguous()))):
+        _typed(t, "dt B C", dt, B, C)
+        _typed(f32, "A D dt_bias state", A, D, dt_bias, state)
+        _dense("A D dt_bias state", A, D, dt_bias, state)
+        _on(x, dt, A, B, C, D, dt_bias, state)
+        _shaped("dt", dt, shape[:-1])
+        _shaped("B", B, shape[:-2] + bshape[-2:])
+        _shaped("C", C, bshape)
+        raise ValueError("A, D and dt_bias must be [H], state [n_slots, H, N, P]")
     return H, G, N, P, _rows("x", x, lead), _rows("dt", dt, lead), _rows("B", B, lead), _rows("C", C, lead)
 
 
@@ -687,60 +738,62 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
     updated in place; slots, ctx [R] int32.  page_size > 0: the state at every
     multiple of it goes to pages [n_pages, H, N, P] through block_table
     [R, blocks] int32.  Returns y like x."""
-    import torch
-    lead = x.dim() - 2
-    if lead not in (1, 2):
-        raise ValueError("x must be [rows, H, P] or [B, T, H, P]")
-    R, rows = _requests(x, lead, state, slots, ctx, cu)
-    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead)
+    torch = _torch or _init()
     code = _dtype_code(x)
-    _on(x.device, slots, ctx, cu, block_table, pages, y, workspace)
-    stride = n_pages = 0
+    lead = x.dim() - 2
+    if lead not in (1, 2) or B.dim() != lead + 2:
+        raise ValueError("x must be [rows, H, P] or [B, T, H, P], B and C [.., G, N]")
+    d = x.get_device()
+    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d)
+    R, rows = _requests(x, lead, slots, ctx, cu, d)
+    width = n_pages = 0
     if page_size:
         if block_table is None or pages is None:
             raise ValueError("page_size needs block_table and pages")
-        _typed(torch.int32, block_table=block_table)
-        _typed(torch.float32, pages=pages)
-        if block_table.dim() != 2 or block_table.shape[0] != R:
+        _typed(torch.int32, "block_table", block_table)
+        _typed(torch.float32, "pages", pages)
+        _dense("block_table pages", block_table, pages)
+        _on(x, block_table, pages)
+        if block_table.dim() != 2 or block_table.size(0) != R:
             raise ValueError("block_table must be [R, blocks]")
-        n_pages, stride = pages.shape[0], block_table.shape[1]
+        n_pages, width = pages.size(0), block_table.size(1)
         _shaped("pages", pages, (n_pages, H, N, P))
-    if y is None:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-    _typed(x.dtype, y=y)
-    _shaped("y", y, x.shape)
-    with _Call(x.device, stream) as st:
-        ws = kda_ssm_scan_workspace_size(R, rows, H, G, N, P, code)
-        if ws == (1 << 64) - 1:
-            raise KdaError(2, "kda_ssm_scan_workspace_size")
-        if ws > 0 and workspace is None:
-            workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
-        wbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        _check(kda_ssm_scan(x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(A), B.data_ptr(), bs, C.data_ptr(), cs, _ptr(D),
-                            _ptr(dt_bias), 1 if softplus else 0, _ptr(state), 0 if state is None else state.shape[0],
-                            _ptr(slots), _ptr(ctx), _ptr(cu), _ptr(block_table), stride, _ptr(pages), n_pages, page_size,
-                            y.data_ptr(), _rows("y", y, lead), R, rows, H, G, N, P, code, _ptr(workspace), wbytes, st),
-               "kda_ssm_scan")
+    else:
+        block_table = pages = None
+    y, ys = _output(x, y, lead, H * P)
+    lib = load_library()
+    ws = lib.kda_ssm_scan_workspace_size(R, rows, H, G, N, P, code)
+    if ws == (1 << 64) - 1:
+        raise KdaError(2, "kda_ssm_scan_workspace_size")
+    wbytes = 0
+    if ws > 0 and workspace is None:
+        workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
+    if workspace is not None:
+        _dense("workspace", workspace)
+        _on(x, workspace)
+        wbytes = workspace.numel() * workspace.element_size()
+    _launch(lib.kda_ssm_scan, "kda_ssm_scan", d, stream,
+            (x.data_ptr(), xs, dt.data_ptr(), ds, A.data_ptr(), B.data_ptr(), bs, C.data_ptr(), cs, _at(D), _at(dt_bias),
+             1 if softplus else 0, _at(state), 0 if state is None else state.size(0), _at(slots), _at(ctx), _at(cu),
+             _at(block_table), width, _at(pages), n_pages, page_size, y.data_ptr(), ys, R, rows, H, G, N, P, code,
+             _at(workspace), wbytes))
     return y
 
 
 def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, softplus=True, slots=None, y=None, stream=None):
     """ssm_scan for one new token of each of R sequences: x [R, H, P], dt [R, H],
     B, C [R, G, N]; state: pool [n_slots, H, N, P] fp32, updated in place.  Returns y [R, H, P]."""
-    import torch
-    if x.dim() != 3:
-        raise ValueError("x must be [R, H, P]")
-    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, 1)
-    R = x.shape[0]
-    _typed(torch.int32, slots=slots)
-    _shaped("slots", slots, (R,))
-    _on(x.device, slots, y)
-    if y is None:
-        y = torch.empty(R, H, P, dtype=x.dtype, device=x.device)
-    _typed(x.dtype, y=y)
-    _shaped("y", y, (R, H, P))
-    with _Call(x.device, stream) as st:
-        _check(kda_ssm_step(x.data_ptr(), xs, dt.data_ptr(), ds, _ptr(A), B.data_ptr(), bs, C.data_ptr(), cs, _ptr(D),
-                            _ptr(dt_bias), 1 if softplus else 0, _ptr(state), state.shape[0], _ptr(slots), y.data_ptr(),
-                            _rows("y", y, 1), R, H, G, N, P, _dtype_code(x), st), "kda_ssm_step")
+    torch = _torch or _init()
+    code = _dtype_code(x)
+    if x.dim() != 3 or B.dim() != 3:
+        raise ValueError("x must be [R, H, P], B and C [R, G, N]")
+    R, d = x.size(0), x.get_device()
+    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, 1, d)
+    if not _good_slots(slots, R, d, torch.int32):
+        _on(x, slots)
+        _bad_requests(slots, None, None, R)
+    y, ys = _output(x, y, 1, H * P)
+    _launch(load_library().kda_ssm_step, "kda_ssm_step", d, stream,
+            (x.data_ptr(), xs, dt.data_ptr(), ds, A.data_ptr(), B.data_ptr(), bs, C.data_ptr(), cs, _at(D), _at(dt_bias),
+             1 if softplus else 0, state.data_ptr(), state.size(0), _at(slots), y.data_ptr(), ys, R, H, G, N, P, code))
     return y
