@@ -36,7 +36,7 @@ struct ConvArgs {
   int64_t x_stride, y_stride;
   int C, K, d;  // d: head dimension (norm, head-major output), else 0
   int bf16, silu, norm, head_major;
-  int vec;  // every access of a channel vector is 16-byte aligned
+  int vec;  // four channels can be moved at once everywhere
   float eps;
 };
 

@@ -61,12 +61,12 @@ kda_status_t check_conv(const void *x, int64_t x_stride, const void *w, const vo
   return KDA_OK;
 }
 
-// Whether a thread's 16 bytes of channels can be moved at once everywhere.
+// Whether a thread's four channels can be moved at once everywhere.
 bool conv_vectors(const kda::ConvArgs &a) {
-  const size_t e = a.bf16 ? 2 : 4;
-  if (a.C % (16 / e) != 0 || (a.x_stride * e) % 16 != 0) return false;
-  if (!a.head_major && (a.y_stride * e) % 16 != 0) return false;
-  return aligned16(a.x) && aligned16(a.y) && aligned16(a.state) && aligned16(a.w) && aligned16(a.bias);
+  const size_t bytes = a.bf16 ? 8 : 16;
+  auto fits = [&](const void *p) { return aligned_to(p, bytes); };
+  return a.C % 4 == 0 && a.x_stride % 4 == 0 && (a.head_major || a.y_stride % 4 == 0) && fits(a.x) && fits(a.y) &&
+         fits(a.state) && fits(a.w) && fits(a.bias);
 }
 
 }  // namespace

@@ -3,12 +3,13 @@
 // projections): K taps a channel, Swish, L2 norm of each head.
 //
 // Bytes bound both: an input element is read once and an output element
-// written once for about 2 K + 8 operations.  A thread owns a vector of V
-// channels (16 bytes) and walks down a tile of rows with the last K - 1 inputs
-// in registers, so an input is loaded once a tile (plus K - 1 rows of halo).
-// Tiles are cut over the packed rows, not over the sequences, so the grid
-// needs no lengths on the host; a tile walks through the sequences that it
-// meets.
+// written once for about 2 K + 8 operations.  A thread owns four channels (8 or
+// 16 bytes; a warp moves 256 or 512 bytes of a row) and walks down a tile of rows
+// with the last K - 1 inputs in registers, so an input is loaded once a tile (plus
+// K - 1 rows of halo), sixteen rows ahead of their use.  Eight channels a thread took
+// 168 registers, which left 3 blocks an SM and 1.8 TB/s at 65,536 x 4,352 bf16.
+// Tiles are cut over the packed rows, not over the sequences, so the grid needs no
+// lengths on the host; a tile walks through the sequences that it meets.
 //
 // The pool is read where a sequence starts and written where it ends, which
 // may be different tiles: the tile with the last row therefore also computes
@@ -20,87 +21,173 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int V = 4;  // channels of a thread
 
+// Four elements as loaded.
 template <typename T>
-constexpr int kVec = 16 / (int)sizeof(T);
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 u;
+  __device__ __forceinline__ float2 lo() const { return pair(u.x); }
+  __device__ __forceinline__ float2 hi() const { return pair(u.y); }
+  static __device__ __forceinline__ float2 pair(uint32_t w) {
+    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+  }
+};
+template <>
+struct Raw<float> {
+  float4 u;
+  __device__ __forceinline__ float2 lo() const { return make_float2(u.x, u.y); }
+  __device__ __forceinline__ float2 hi() const { return make_float2(u.z, u.w); }
+};
 
-// V elements from p (16-byte aligned if VEC), zeros behind the first n.
+struct F4 {
+  float2 a, b;
+};
+template <typename T>
+__device__ __forceinline__ F4 widen(const Raw<T> &r) { return F4{r.lo(), r.hi()}; }
+
+// Four elements from p (aligned to them if VEC); zeros behind the first n.
 template <typename T, bool VEC>
-__device__ __forceinline__ void load_v(const T *p, int n, float (&v)[kVec<T>]) {
+__device__ __forceinline__ Raw<T> load4(const T *p, int n) {
+  union { Raw<T> r; T t[V]; };
   if constexpr (VEC) {
-    union { uint4 u; T t[kVec<T>]; } b;
-    b.u = n > 0 ? *reinterpret_cast<const uint4 *>(p) : make_uint4(0, 0, 0, 0);
+    if (n > 0) return *reinterpret_cast<const Raw<T> *>(p);
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) v[j] = as_float(b.t[j]);
+    for (int j = 0; j < V; ++j) t[j] = as_type<T>(0.f);
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) v[j] = j < n ? as_float(p[j]) : 0.f;
+    for (int j = 0; j < V; ++j) t[j] = j < n ? p[j] : as_type<T>(0.f);
   }
+  return r;
 }
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_v(T *p, int n, const float (&v)[kVec<T>]) {
+__device__ __forceinline__ void store4(T *p, int n, const F4 &v) {
+  union { Raw<T> r; T t[V]; };
+  t[0] = as_type<T>(v.a.x); t[1] = as_type<T>(v.a.y); t[2] = as_type<T>(v.b.x); t[3] = as_type<T>(v.b.y);
   if constexpr (VEC) {
-    union { uint4 u; T t[kVec<T>]; } b;
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) b.t[j] = as_type<T>(v[j]);
-    if (n > 0) *reinterpret_cast<uint4 *>(p) = b.u;
+    if (n > 0) *reinterpret_cast<Raw<T> *>(p) = r;
   } else {
 #pragma unroll
-    for (int j = 0; j < kVec<T>; ++j)
-      if (j < n) p[j] = as_type<T>(v[j]);
+    for (int j = 0; j < V; ++j)
+      if (j < n) p[j] = t[j];
   }
 }
 
-// v Sigmoid(v).  The fast forms are off by a few 2^-22, far below a bf16 step.
-__device__ __forceinline__ float swish(float v, __nv_bfloat16) { return __fdividef(v, 1.f + __expf(-v)); }
-__device__ __forceinline__ float swish(float v, float) { return v / (1.f + expf(-v)); }
+// v Sigmoid(v).  The bf16 form takes the hardware's 2^x and 1/x (2^-22 relative, far
+// below a bf16 step; results below the normal range are 0): nine instructions a pair.
+__device__ __forceinline__ float2 swish(float2 v, __nv_bfloat16) {
+  float2 e = __fmul2_rn(v, make_float2(-1.4426950408889634f, -1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+  e = __fadd2_rn(e, make_float2(1.f, 1.f));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.x));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(e.y));
+  return __fmul2_rn(v, e);
+}
+__device__ __forceinline__ float2 swish(float2 v, float) {
+  return make_float2(v.x / (1.f + expf(-v.x)), v.y / (1.f + expf(-v.y)));
+}
 
-template <typename T, int K>
+template <int K>
 struct Taps {
-  float w[K][kVec<T>], b[kVec<T>];
+  F4 w[K], b;
 };
 
 template <typename T, int K, bool VEC>
-__device__ __forceinline__ void load_taps(const ConvArgs &a, int c0, int n, Taps<T, K> &t) {
+__device__ __forceinline__ Taps<K> load_taps(const ConvArgs &a, int c0, int n) {
+  Taps<K> t;
+  union { Raw<T> r[K]; T e[V * K]; };  // channel by channel, as in memory
   const T *w = (const T *)a.w + (int64_t)c0 * K;
+  union { Raw<T> rb; T eb[V]; };
+#pragma unroll
+  for (int i = 0; i < K; ++i) r[i] = load4<T, VEC>(w + V * i, VEC ? n : n * K - V * i);
+  rb = load4<T, VEC>((const T *)a.bias + c0, a.bias ? n : 0);
 #pragma unroll
   for (int i = 0; i < K; ++i)
-#pragma unroll
-    for (int j = 0; j < kVec<T>; ++j) t.w[i][j] = j < n ? as_float(w[j * K + i]) : 0.f;
-#pragma unroll
-  for (int j = 0; j < kVec<T>; ++j) t.b[j] = a.bias && j < n ? as_float(((const T *)a.bias)[c0 + j]) : 0.f;
+    t.w[i] = F4{make_float2(as_float(e[i]), as_float(e[K + i])), make_float2(as_float(e[2 * K + i]), as_float(e[3 * K + i]))};
+  t.b = F4{make_float2(as_float(eb[0]), as_float(eb[1])), make_float2(as_float(eb[2]), as_float(eb[3]))};
+  return t;
 }
+
+// A thread's own queue of its tile's rows in flight, in shared memory: kDepth rows
+// asynchronous copies ahead, across the borders of sequences, without a register or a
+// barrier for them (every thread reads only what it asked for).  65,536 x 4,352 bf16:
+// 283 us with four rows ahead in registers.
+constexpr int kGroup = 4, kGroups = 4, kDepth = kGroup * kGroups;
+template <typename T>
+struct Queue {
+  Raw<T> *mine;    // [kDepth][kThreads], this thread's column
+  const T *from;   // the next row to ask for
+  int64_t xs;
+  int left;        // rows of the tile that are not asked for yet
+  int i;           // rows taken
+  // Ask for the next kGroup rows, into the places of group g.
+  __device__ __forceinline__ void ask(int g) {
+#pragma unroll
+    for (int b = 0; b < kGroup; ++b, from += xs)
+      if (b < left) {
+        const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + (g * kGroup + b) * kThreads);
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"((int)sizeof(Raw<T>)) : "memory");
+      }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    left -= kGroup;
+  }
+  // Rows from p on, `rows` of them.
+  __device__ __forceinline__ void begin(const T *p, int rows) {
+    asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may still land in the places
+    from = p;
+    left = rows;
+    i = 0;
+#pragma unroll
+    for (int g = 0; g < kGroups; ++g) ask(g);
+  }
+  // The oldest group that was asked for has arrived.
+  __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory"); }
+  __device__ __forceinline__ Raw<T> at(int k) const { return mine[(k % kDepth) * kThreads]; }
+  __device__ __forceinline__ Raw<T> next() {
+    if (i % kGroup == 0) wait();
+    return at(i);
+  }
+  // After a row was used.
+  __device__ __forceinline__ void taken() {
+    if (++i % kGroup == 0) ask((i / kGroup - 1) % kGroups);
+  }
+};
 
 // Output of one row from its K inputs, oldest first.  A head's channels lie in
 // d / V neighbouring lanes, so its norm is a butterfly over them: every lane of
 // the warp must come here.
 template <typename T, int K>
-__device__ __forceinline__ void conv_row(const ConvArgs &a, const Taps<T, K> &t, const float *const (&u)[K],
-                                         float (&o)[kVec<T>]) {
-  constexpr int V = kVec<T>;
-  float ss = 0.f;
+__device__ __forceinline__ F4 conv_row(const ConvArgs &a, const Taps<K> &t, const F4 (&u)[K]) {
+  F4 o = t.b;
 #pragma unroll
-  for (int j = 0; j < V; ++j) {
-    float v = t.b[j];
-#pragma unroll
-    for (int i = 0; i < K; ++i) v = fmaf(t.w[i][j], u[i][j], v);
-    if (a.silu) v = swish(v, T());
-    o[j] = v;
-    ss = fmaf(v, v, ss);
+  for (int i = 0; i < K; ++i) {
+    o.a = __ffma2_rn(t.w[i].a, u[i].a, o.a);
+    o.b = __ffma2_rn(t.w[i].b, u[i].b, o.b);
+  }
+  if (a.silu) {
+    o.a = swish(o.a, T());
+    o.b = swish(o.b, T());
   }
   if (a.norm) {
+    float2 q = __ffma2_rn(o.a, o.a, __fmul2_rn(o.b, o.b));
+    float ss = q.x + q.y;
     for (int off = 1; off < a.d / V; off <<= 1) ss += __shfl_xor_sync(~0u, ss, off);
     const float f = 1.f / sqrtf(ss + a.eps);
-#pragma unroll
-    for (int j = 0; j < V; ++j) o[j] *= f;
+    o.a = __fmul2_rn(o.a, make_float2(f, f));
+    o.b = __fmul2_rn(o.b, make_float2(f, f));
   }
+  return o;
 }
 
 template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kThreads) short_conv_kernel(ConvArgs a, int tile) {
-  constexpr int V = kVec<T>;
-  constexpr int NB = 4;  // rows whose loads are in flight together
+__global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int tile) {
+  __shared__ Raw<T> rows_ahead[VEC ? kDepth * kThreads : 1];
+  Queue<T> queue;
+  queue.mine = rows_ahead + (VEC ? threadIdx.x : 0);
   const Requests &q = a.q;
   const int row0 = (int)((int64_t)blockIdx.x * tile);
   const int c0 = (blockIdx.y * kThreads + threadIdx.x) * V;
@@ -123,19 +210,13 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(ConvArgs a, int ti
     row = q.cu[0];
   }
   if (row >= rend) return;
-  Taps<T, K> taps;
-  load_taps<T, K, VEC>(a, c0, n, taps);
-
-  auto put = [&](int rr, const Seq &s, int at, const float (&o)[V]) {
-    T *y = (T *)a.y;
-    if (a.head_major) {
-      const int len = s.end - s.start, h = c0 / a.d;
-      y += (((int64_t)rr * (a.C / a.d) + h) * len + (at - s.start)) * a.d + c0 % a.d;
-    } else {
-      y += (int64_t)at * a.y_stride + c0;
-    }
-    store_v<T, VEC>(y, n, o);
+  queue.xs = xs;
+  auto ahead = [&]() {
+    if (VEC && row < rend) queue.begin(x + row * xs, n > 0 ? rend - row : 0);
   };
+  ahead();
+  const Taps<K> taps = load_taps<T, K, VEC>(a, c0, n);
+  const Raw<T> none = load4<T, VEC>(x, 0);
 
   while (row < rend) {
     while (r < q.R && q.cu && q.cu[r + 1] <= row) ++r;
@@ -145,76 +226,80 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(ConvArgs a, int ti
     if (!s.ok || row < s.start) {  // (row < start: offsets that decrease)
       row = max(stop, row + 1);
       ++r;
+      ahead();
       continue;
     }
     const bool carry = pool && s.ctx > 0, here = s.end <= rend;
     T *entry = pool ? pool + (int64_t)s.slot * (K - 1) * a.C : nullptr;
-    float h[K - 1][V];  // the K - 1 inputs before `row`, oldest first
+    // where the sequence's row 0 goes, and the step from row to row
+    T *y = (T *)a.y;
+    int64_t ys = a.y_stride;
+    if (a.head_major) {
+      ys = a.d;
+      y += ((int64_t)r * (a.C / a.d) + c0 / a.d) * (s.end - s.start) * a.d + c0 % a.d;
+    } else {
+      y += s.start * ys + c0;
+    }
+    F4 h[K - 1];  // the K - 1 inputs before `row`, oldest first
     // (a sequence that reads the pool and ends in a later tile: that tile computes the outputs
     // that need it)
 #pragma unroll
     for (int i = 0; i < K - 1; ++i) {
       const int at = row - (K - 1) + i;
-      if (at >= s.start) {
-        load_v<T, VEC>(x + at * xs, n, h[i]);
-      } else if (carry && here) {
-        load_v<T, VEC>(entry + (int64_t)(at - s.start + K - 1) * a.C, n, h[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) h[i][j] = 0.f;
-      }
+      const F4 zero = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+      h[i] = at >= s.start    ? widen(load4<T, VEC>(x + at * xs, n))
+             : carry && here ? widen(load4<T, VEC>(entry + (int64_t)(at - s.start + K - 1) * a.C, n))
+                             : zero;
     }
     if (carry && here && row > s.start) {  // its first rows, in earlier tiles
       for (int at = s.start; at < min(row, s.start + K - 1); ++at) {
-        float u[K][V], o[V];
-        const float *up[K];
+        F4 u[K];
 #pragma unroll
         for (int i = 0; i < K; ++i) {
           const int p = at - (K - 1) + i - s.start;
-          load_v<T, VEC>(p >= 0 ? x + (s.start + p) * xs : entry + (int64_t)(p + K - 1) * a.C, n, u[i]);
-          up[i] = u[i];
+          u[i] = widen(load4<T, VEC>(p >= 0 ? x + (s.start + p) * xs : entry + (int64_t)(p + K - 1) * a.C, n));
         }
-        conv_row<T, K>(a, taps, up, o);
-        put(r, s, at, o);
+        store4<T, VEC>(y + (at - s.start) * ys, n, conv_row<T, K>(a, taps, u));
       }
     }
     const int first = carry && !here ? s.start + K - 1 : row;  // rows before it are another tile's
+    T *yr = y + (row - s.start) * ys;
+    // one row: its inputs are h and `in`, which then moves into h
+    auto step = [&](const Raw<T> &in, T *to, bool keep) {
+      F4 w[K];
+#pragma unroll
+      for (int i = 0; i < K - 1; ++i) w[i] = h[i];
+      w[K - 1] = widen(in);
+      const F4 o = conv_row<T, K>(a, taps, w);
+      if (keep) store4<T, VEC>(to, n, o);
+#pragma unroll
+      for (int i = 0; i < K - 1; ++i) h[i] = w[i + 1];
+    };
     while (row < stop) {
-      float u[NB][V];
+      if (VEC && queue.i % kGroup == 0 && row + kGroup <= stop && row >= first) {  // a whole group
+        queue.wait();
 #pragma unroll
-      for (int b = 0; b < NB; ++b) load_v<T, VEC>(x + (row + b) * xs, row + b < stop ? n : 0, u[b]);
-#pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        if (row + b < stop) {
-          float o[V];
-          const float *up[K];
-#pragma unroll
-          for (int i = 0; i < K; ++i) up[i] = b + i < K - 1 ? h[b + i < K - 1 ? b + i : 0] : u[b + i - (K - 1) >= 0 ? b + i - (K - 1) : 0];
-          conv_row<T, K>(a, taps, up, o);
-          if (row + b >= first) put(r, s, row + b, o);
-        }
-      }
-      const int nb = min(NB, stop - row);
-      if (nb == NB) {
-#pragma unroll
-        for (int i = 0; i < K - 1; ++i)
-#pragma unroll
-          for (int j = 0; j < V; ++j) h[i][j] = u[NB - (K - 1) + i][j];
+        for (int b = 0; b < kGroup; ++b, yr += ys) step(n > 0 ? queue.at(queue.i + b) : none, yr, true);
+        row += kGroup;
+        queue.i += kGroup - 1;
+        queue.taken();
       } else {
-        for (int b = 0; b < nb; ++b) {
-#pragma unroll
-          for (int i = 0; i + 1 < K - 1; ++i)
-#pragma unroll
-            for (int j = 0; j < V; ++j) h[i][j] = h[i + 1][j];
-#pragma unroll
-          for (int j = 0; j < V; ++j) h[K - 2][j] = b == 0 ? u[0][j] : b == 1 ? u[1][j] : u[2][j];
+        Raw<T> in = none;
+        if constexpr (VEC) {
+          in = queue.next();
+          if (n <= 0) in = none;
+        } else {
+          in = load4<T, VEC>(x + row * xs, n);
         }
+        step(in, yr, row >= first);
+        if (VEC) queue.taken();
+        ++row;
+        yr += ys;
       }
-      row += nb;
     }
     if (here && pool) {
 #pragma unroll
-      for (int i = 0; i < K - 1; ++i) store_v<T, VEC>(entry + (int64_t)i * a.C, n, h[i]);
+      for (int i = 0; i < K - 1; ++i) store4<T, VEC>(entry + (int64_t)i * a.C, n, h[i]);
     }
     ++r;
   }
@@ -222,7 +307,6 @@ __global__ void __launch_bounds__(kThreads) short_conv_kernel(ConvArgs a, int ti
 
 template <typename T, int K, bool VEC>
 __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(ConvArgs a) {
-  constexpr int V = kVec<T>;
   const int r = blockIdx.x;
   const int c0 = (blockIdx.y * kThreads + threadIdx.x) * V;
   const int n = min(V, a.C - c0);
@@ -233,19 +317,14 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(ConvArgs a) {
     return;
   }
   T *entry = (T *)a.state + (int64_t)slot * (K - 1) * a.C + c0;
-  float u[K][V], o[V];
-  const float *up[K];
+  F4 u[K];
 #pragma unroll
-  for (int i = 0; i < K - 1; ++i) load_v<T, VEC>(entry + (int64_t)i * a.C, n, u[i]);
-  load_v<T, VEC>((const T *)a.x + r * a.x_stride + c0, n, u[K - 1]);
-  Taps<T, K> taps;
-  load_taps<T, K, VEC>(a, c0, n, taps);
+  for (int i = 0; i < K - 1; ++i) u[i] = widen(load4<T, VEC>(entry + (int64_t)i * a.C, n));
+  u[K - 1] = widen(load4<T, VEC>((const T *)a.x + r * a.x_stride + c0, n));
+  const Taps<K> taps = load_taps<T, K, VEC>(a, c0, n);
+  store4<T, VEC>((T *)a.y + r * a.y_stride + c0, n, conv_row<T, K>(a, taps, u));
 #pragma unroll
-  for (int i = 0; i < K; ++i) up[i] = u[i];
-  conv_row<T, K>(a, taps, up, o);
-  store_v<T, VEC>((T *)a.y + r * a.y_stride + c0, n, o);
-#pragma unroll
-  for (int i = 0; i < K - 1; ++i) store_v<T, VEC>(entry + (int64_t)i * a.C, n, u[i + 1]);
+  for (int i = 0; i < K - 1; ++i) store4<T, VEC>(entry + (int64_t)i * a.C, n, u[i + 1]);
 }
 
 // f(T, K, VEC) for the call's type, taps and alignment.
@@ -262,13 +341,21 @@ cudaError_t dispatch(const ConvArgs &a, F f) {
   return cudaErrorInvalidValue;
 }
 
+// Rows of a tile: 64, or fewer where that leaves the SMs with less than eight blocks each.
+int conv_tile(const ConvArgs &a) {
+  const int64_t columns = (a.C + kThreads * V - 1) / (kThreads * V);
+  int tile = 64;
+  while (tile > 8 && columns * ((a.q.rows + tile - 1) / tile) < 8 * 148) tile /= 2;
+  return tile;
+}
+
 struct RunConv {
   const ConvArgs &a;
   cudaStream_t st;
   template <typename T, int K, bool VEC>
   cudaError_t run() const {
-    const int tile = 16;
-    const dim3 grid((unsigned)(((int64_t)a.q.rows + tile - 1) / tile), (a.C + kThreads * kVec<T> - 1) / (kThreads * kVec<T>));
+    const int tile = conv_tile(a);
+    const dim3 grid((unsigned)(((int64_t)a.q.rows + tile - 1) / tile), (a.C + kThreads * V - 1) / (kThreads * V));
     short_conv_kernel<T, K, VEC><<<grid, kThreads, 0, st>>>(a, tile);
     return cudaGetLastError();
   }
@@ -279,7 +366,7 @@ struct RunStep {
   cudaStream_t st;
   template <typename T, int K, bool VEC>
   cudaError_t run() const {
-    const dim3 grid(a.q.R, (a.C + kThreads * kVec<T> - 1) / (kThreads * kVec<T>));
+    const dim3 grid(a.q.R, (a.C + kThreads * V - 1) / (kThreads * V));
     short_conv_step_kernel<T, K, VEC><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
