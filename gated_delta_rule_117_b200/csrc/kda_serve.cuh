@@ -14,7 +14,7 @@ namespace kda {
 // The requests of a call: see "Packed requests" in include/kda.h.
 struct Requests {
   const int *cu, *ctx, *slots;
-  int R, rows, n_slots;  // n_slots 0: no pool
+  int R, rows, T, n_slots;  // T: tokens of a sequence without cu; n_slots 0: no pool
   unsigned *status;
 };
 
@@ -35,6 +35,7 @@ struct ConvArgs {
   void *state, *y;
   int64_t x_stride, y_stride;
   int C, K, d;  // d: head dimension (norm, head-major output), else 0
+  int log2_d, heads;
   int bf16, silu, norm, head_major;
   int vec;  // four channels can be moved at once everywhere
   float eps;
@@ -82,9 +83,8 @@ __device__ __forceinline__ Seq seq_of(const Requests &q, int r, bool tell) {
     s.start = q.cu[r];
     s.end = q.cu[r + 1];
   } else {
-    const int T = q.rows / q.R;
-    s.start = r * T;
-    s.end = s.start + T;
+    s.start = r * q.T;
+    s.end = s.start + q.T;
   }
   s.slot = q.slots ? q.slots[r] : r;
   s.ctx = q.ctx ? max(q.ctx[r], 0) : 0;

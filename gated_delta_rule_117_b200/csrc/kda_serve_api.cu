@@ -61,6 +61,14 @@ kda_status_t check_conv(const void *x, int64_t x_stride, const void *w, const vo
   return KDA_OK;
 }
 
+void set_shape(kda::ConvArgs &a, int C, int K, int head_dim) {
+  a.C = C;
+  a.K = K;
+  a.d = supported_d(head_dim) ? head_dim : 0;
+  a.log2_d = a.d == 16 ? 4 : a.d == 32 ? 5 : a.d == 64 ? 6 : 7;
+  a.heads = a.d ? C / a.d : 0;
+}
+
 // Whether a thread's four channels can be moved at once everywhere.
 bool conv_vectors(const kda::ConvArgs &a) {
   const size_t bytes = a.bf16 ? 8 : 16;
@@ -121,11 +129,11 @@ kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *w, cons
   st = check_device();
   if (st != KDA_OK) return st;
   kda::ConvArgs a;
-  a.q = kda::Requests{cu, ctx, slots, R, rows, n_slots, kda::device_status_ptr()};
+  a.q = kda::Requests{cu, ctx, slots, R, rows, rows / R, n_slots, kda::device_status_ptr()};
   if (!a.q.status) return KDA_ERR_CUDA;
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
   a.x_stride = x_stride; a.y_stride = y_stride;
-  a.C = C; a.K = K; a.d = head_dim;
+  set_shape(a, C, K, head_dim);
   a.bf16 = dtype == KDA_DTYPE_BF16;
   a.silu = (flags & KDA_CONV_SILU) != 0;
   a.norm = (flags & KDA_CONV_L2NORM) != 0;
@@ -153,11 +161,11 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
   st = check_device();
   if (st != KDA_OK) return st;
   kda::ConvArgs a;
-  a.q = kda::Requests{nullptr, nullptr, slots, R, R, n_slots, kda::device_status_ptr()};
+  a.q = kda::Requests{nullptr, nullptr, slots, R, R, 1, n_slots, kda::device_status_ptr()};
   if (!a.q.status) return KDA_ERR_CUDA;
   a.x = x; a.w = w; a.bias = bias; a.state = state; a.y = y;
   a.x_stride = x_stride; a.y_stride = y_stride;
-  a.C = C; a.K = K; a.d = head_dim;
+  set_shape(a, C, K, head_dim);
   a.bf16 = dtype == KDA_DTYPE_BF16;
   a.silu = (flags & KDA_CONV_SILU) != 0;
   a.norm = (flags & KDA_CONV_L2NORM) != 0;
@@ -241,7 +249,7 @@ kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64
   const size_t need = kda::ssm_scan_workspace(R, rows, H, G, N, P, dtype == KDA_DTYPE_BF16);
   if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   kda::SsmArgs a;
-  a.q = kda::Requests{cu, ctx, slots, R, rows, n_slots, nullptr};
+  a.q = kda::Requests{cu, ctx, slots, R, rows, rows / R, n_slots, nullptr};
   a.x = x; a.dt = dt; a.A = A; a.B = Bm; a.C = Cm; a.D = D; a.dt_bias = dt_bias;
   a.x_stride = x_stride; a.dt_stride = dt_stride; a.b_stride = b_stride; a.c_stride = c_stride;
   a.y = y; a.y_stride = y_stride;
@@ -274,7 +282,7 @@ kda_status_t kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64
   if ((int64_t)R * H > INT32_MAX) return KDA_ERR_SHAPE;
   if (!state) return KDA_ERR_INVALID_ARG;
   kda::SsmArgs a;
-  a.q = kda::Requests{nullptr, nullptr, slots, R, R, n_slots, nullptr};
+  a.q = kda::Requests{nullptr, nullptr, slots, R, R, 1, n_slots, nullptr};
   a.x = x; a.dt = dt; a.A = A; a.B = Bm; a.C = Cm; a.D = D; a.dt_bias = dt_bias;
   a.x_stride = x_stride; a.dt_stride = dt_stride; a.b_stride = b_stride; a.c_stride = c_stride;
   a.y = y; a.y_stride = y_stride;

@@ -21,6 +21,7 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
+constexpr int kBlocks = 6;  // an SM: 80 registers (7 and 8 spill: 225 and 253 us against 216 at 65,536 x 4,352 bf16)
 constexpr int V = 4;  // channels of a thread
 
 // Four elements as loaded.
@@ -48,6 +49,14 @@ struct F4 {
 template <typename T>
 __device__ __forceinline__ F4 widen(const Raw<T> &r) { return F4{r.lo(), r.hi()}; }
 
+__device__ __forceinline__ Raw<__nv_bfloat16> narrow(const F4 &v, __nv_bfloat16) {
+  const __nv_bfloat162 a = __float22bfloat162_rn(v.a), b = __float22bfloat162_rn(v.b);
+  return Raw<__nv_bfloat16>{make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&b))};
+}
+__device__ __forceinline__ Raw<float> narrow(const F4 &v, float) {
+  return Raw<float>{make_float4(v.a.x, v.a.y, v.b.x, v.b.y)};
+}
+
 // Four elements from p (aligned to them if VEC); zeros behind the first n.
 template <typename T, bool VEC>
 __device__ __forceinline__ Raw<T> load4(const T *p, int n) {
@@ -66,7 +75,7 @@ __device__ __forceinline__ Raw<T> load4(const T *p, int n) {
 template <typename T, bool VEC>
 __device__ __forceinline__ void store4(T *p, int n, const F4 &v) {
   union { Raw<T> r; T t[V]; };
-  t[0] = as_type<T>(v.a.x); t[1] = as_type<T>(v.a.y); t[2] = as_type<T>(v.b.x); t[3] = as_type<T>(v.b.y);
+  r = narrow(v, T());
   if constexpr (VEC) {
     if (n > 0) *reinterpret_cast<Raw<T> *>(p) = r;
   } else {
@@ -90,6 +99,10 @@ __device__ __forceinline__ float2 swish(float2 v, __nv_bfloat16) {
 __device__ __forceinline__ float2 swish(float2 v, float) {
   return make_float2(v.x / (1.f + expf(-v.x)), v.y / (1.f + expf(-v.y)));
 }
+
+// 1 / sqrt(v); the bf16 form is off by at most two units in the last place.
+__device__ __forceinline__ float inverse_root(float v, __nv_bfloat16) { return rsqrtf(v); }
+__device__ __forceinline__ float inverse_root(float v, float) { return 1.f / sqrtf(v); }
 
 template <int K>
 struct Taps {
@@ -123,15 +136,17 @@ struct Queue {
   const T *from;   // the next row to ask for
   int64_t xs;
   int left;        // rows of the tile that are not asked for yet
-  int i;           // rows taken
-  // Ask for the next kGroup rows, into the places of group g.
-  __device__ __forceinline__ void ask(int g) {
+  int i;           // rows taken of the oldest group
+  int head;        // its first place
+  // Ask for the next kGroup rows, into the places from `to` on.
+  __device__ __forceinline__ void ask(int to) {
+    uint32_t p = (uint32_t)__cvta_generic_to_shared(mine + to);
 #pragma unroll
     for (int b = 0; b < kGroup; ++b, from += xs)
-      if (b < left) {
-        const uint32_t to = (uint32_t)__cvta_generic_to_shared(mine + (g * kGroup + b) * kThreads);
-        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(to), "l"(from), "n"((int)sizeof(Raw<T>)) : "memory");
-      }
+      if (b < left)
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(p + b * kThreads * (int)sizeof(Raw<T>)), "l"(from),
+                     "n"((int)sizeof(Raw<T>))
+                     : "memory");
     asm volatile("cp.async.commit_group;" ::: "memory");
     left -= kGroup;
   }
@@ -140,20 +155,19 @@ struct Queue {
     asm volatile("cp.async.wait_all;" ::: "memory");  // nothing may still land in the places
     from = p;
     left = rows;
-    i = 0;
+    i = head = 0;
 #pragma unroll
-    for (int g = 0; g < kGroups; ++g) ask(g);
+    for (int g = 0; g < kGroups; ++g) ask(g * kGroup * kThreads);
   }
   // The oldest group that was asked for has arrived.
   __device__ __forceinline__ void wait() const { asm volatile("cp.async.wait_group %0;" ::"n"(kGroups - 1) : "memory"); }
-  __device__ __forceinline__ Raw<T> at(int k) const { return mine[(k % kDepth) * kThreads]; }
-  __device__ __forceinline__ Raw<T> next() {
-    if (i % kGroup == 0) wait();
-    return at(i);
-  }
-  // After a row was used.
-  __device__ __forceinline__ void taken() {
-    if (++i % kGroup == 0) ask((i / kGroup - 1) % kGroups);
+  // Row b of it.
+  __device__ __forceinline__ Raw<T> row(int b) const { return mine[head + b * kThreads]; }
+  // The group is used up: its places take the next rows.
+  __device__ __forceinline__ void next_group() {
+    ask(head);
+    i = 0;
+    head = head == (kGroups - 1) * kGroup * kThreads ? 0 : head + kGroup * kThreads;
   }
 };
 
@@ -176,7 +190,7 @@ __device__ __forceinline__ F4 conv_row(const ConvArgs &a, const Taps<K> &t, cons
     float2 q = __ffma2_rn(o.a, o.a, __fmul2_rn(o.b, o.b));
     float ss = q.x + q.y;
     for (int off = 1; off < a.d / V; off <<= 1) ss += __shfl_xor_sync(~0u, ss, off);
-    const float f = 1.f / sqrtf(ss + a.eps);
+    const float f = inverse_root(ss + a.eps, T());
     o.a = __fmul2_rn(o.a, make_float2(f, f));
     o.b = __fmul2_rn(o.b, make_float2(f, f));
   }
@@ -184,7 +198,7 @@ __device__ __forceinline__ F4 conv_row(const ConvArgs &a, const Taps<K> &t, cons
 }
 
 template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int tile) {
+__global__ void __launch_bounds__(kThreads, kBlocks) short_conv_kernel(ConvArgs a, int tile) {
   __shared__ Raw<T> rows_ahead[VEC ? kDepth * kThreads : 1];
   Queue<T> queue;
   queue.mine = rows_ahead + (VEC ? threadIdx.x : 0);
@@ -201,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
     total = min(q.cu[q.R], q.rows);
     r = block_count_le(q.R, [&](int i) { return q.cu[i]; }, row0) - 1;
   } else {
-    r = row0 / (q.rows / q.R);
+    r = row0 / q.T;
   }
   const int rend = min((int64_t)row0 + tile, (int64_t)total);
   int row = row0;
@@ -215,8 +229,12 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
     if (VEC && row < rend) queue.begin(x + row * xs, n > 0 ? rend - row : 0);
   };
   ahead();
+  // the rows before the tile, asked for before it is known whose they are
+  Raw<T> before[K - 1];
+#pragma unroll
+  for (int i = 0; i < K - 1; ++i) before[i] = load4<T, VEC>(x + (row - (K - 1) + i) * xs, row - (K - 1) + i >= 0 ? n : 0);
+  bool at_start = true;
   const Taps<K> taps = load_taps<T, K, VEC>(a, c0, n);
-  const Raw<T> none = load4<T, VEC>(x, 0);
 
   while (row < rend) {
     while (r < q.R && q.cu && q.cu[r + 1] <= row) ++r;
@@ -226,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
     if (!s.ok || row < s.start) {  // (row < start: offsets that decrease)
       row = max(stop, row + 1);
       ++r;
+      at_start = false;
       ahead();
       continue;
     }
@@ -236,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
     int64_t ys = a.y_stride;
     if (a.head_major) {
       ys = a.d;
-      y += ((int64_t)r * (a.C / a.d) + c0 / a.d) * (s.end - s.start) * a.d + c0 % a.d;
+      y += (((int64_t)r * a.heads + (c0 >> a.log2_d)) * q.T << a.log2_d) + (c0 & (a.d - 1));
     } else {
       y += s.start * ys + c0;
     }
@@ -247,10 +266,12 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
     for (int i = 0; i < K - 1; ++i) {
       const int at = row - (K - 1) + i;
       const F4 zero = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-      h[i] = at >= s.start    ? widen(load4<T, VEC>(x + at * xs, n))
+      // (only the tile's first sequence can have begun before it)
+      h[i] = at >= s.start    ? (at_start ? widen(before[i]) : zero)
              : carry && here ? widen(load4<T, VEC>(entry + (int64_t)(at - s.start + K - 1) * a.C, n))
                              : zero;
     }
+    at_start = false;
     if (carry && here && row > s.start) {  // its first rows, in earlier tiles
       for (int at = s.start; at < min(row, s.start + K - 1); ++at) {
         F4 u[K];
@@ -276,27 +297,30 @@ __global__ void __launch_bounds__(kThreads, 8) short_conv_kernel(ConvArgs a, int
       for (int i = 0; i < K - 1; ++i) h[i] = w[i + 1];
     };
     while (row < stop) {
-      if (VEC && queue.i % kGroup == 0 && row + kGroup <= stop && row >= first) {  // a whole group
+      if (VEC && queue.i == 0 && row + kGroup <= stop && row >= first) {  // a whole group
         queue.wait();
 #pragma unroll
-        for (int b = 0; b < kGroup; ++b, yr += ys) step(n > 0 ? queue.at(queue.i + b) : none, yr, true);
+        for (int b = 0; b < kGroup; ++b, yr += ys) step(queue.row(b), yr, true);
         row += kGroup;
-        queue.i += kGroup - 1;
-        queue.taken();
-      } else {
-        Raw<T> in = none;
-        if constexpr (VEC) {
-          in = queue.next();
-          if (n <= 0) in = none;
-        } else {
-          in = load4<T, VEC>(x + row * xs, n);
-        }
-        step(in, yr, row >= first);
-        if (VEC) queue.taken();
+        queue.next_group();
+      } else if constexpr (VEC) {
+        if (queue.i == 0) queue.wait();
+        step(queue.row(queue.i), yr, row >= first);
+        if (++queue.i == kGroup) queue.next_group();
         ++row;
         yr += ys;
+      } else {
+        Raw<T> in[kGroup];  // element by element, a group's loads in flight together
+#pragma unroll
+        for (int b = 0; b < kGroup; ++b) in[b] = load4<T, VEC>(x + (row + b) * xs, row + b < stop ? n : 0);
+#pragma unroll
+        for (int b = 0; b < kGroup; ++b)
+          if (row + b < stop) step(in[b], yr + b * ys, row + b >= first);
+        row += kGroup;
+        yr += kGroup * ys;
       }
     }
+    row = stop;
     if (here && pool) {
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) store4<T, VEC>(entry + (int64_t)i * a.C, n, h[i]);
@@ -341,12 +365,14 @@ cudaError_t dispatch(const ConvArgs &a, F f) {
   return cudaErrorInvalidValue;
 }
 
-// Rows of a tile: 64, or fewer where that leaves the SMs with less than eight blocks each.
+// Rows of a tile: 64, or as few as let all tiles run at once (kBlocks an SM), but 8 at
+// least, as a tile costs about eight rows' instructions to begin.  4,096 x 2,048 with
+// norms: tiles of 16 rows (1,024 of them, a second wave of 136) took 18.3 us, of 20
+// 14 us.
 int conv_tile(const ConvArgs &a) {
-  const int64_t columns = (a.C + kThreads * V - 1) / (kThreads * V);
-  int tile = 64;
-  while (tile > 8 && columns * ((a.q.rows + tile - 1) / tile) < 8 * 148) tile /= 2;
-  return tile;
+  const int64_t columns = (a.C + kThreads * V - 1) / (kThreads * V), at_once = kBlocks * 148;
+  const int64_t tile = (columns * a.q.rows + at_once - 1) / at_once;
+  return (int)(tile >= 64 ? 64 : tile <= 8 ? 8 : (tile + kGroup - 1) / kGroup * kGroup);
 }
 
 struct RunConv {

@@ -34,12 +34,12 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
   __shared__ float sx[TB][P], sy[kOut ? TB : 1][P], sd[TB], sa[TB];
   const int tid = threadIdx.x, p = tid >> 2, quarter = tid & 3;
   const int h = blockIdx.x % a.H;
-  const bool tell = h == 0 && tid == 0;
+  const bool tell = kOut && h == 0 && tid == 0;
   Item it;
   if (!item_of(a.q, blockIdx.x / a.H, seg, tell, it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const int g = h / (a.H / a.G);
-  float S[J][4];  // rows 16 j + 4 quarter + i
+  float2 S[J][2];  // rows 16 j + 4 quarter + 0 .. 3
   const int64_t at = (it.item * a.H + h) * (N * P);
   const float *from = nullptr;
   if (kOut) {
@@ -49,18 +49,26 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
 #pragma unroll
   for (int j = 0; j < J; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) S[j][i] = from ? from[(16 * j + 4 * quarter + i) * P + p] : 0.f;
+    for (int i = 0; i < 2; ++i) {
+      const int n = 16 * j + 4 * quarter + 2 * i;
+      S[j][i] = from ? make_float2(from[n * P + p], from[(n + 1) * P + p]) : make_float2(0.f, 0.f);
+    }
   auto save = [&](float *to) {
 #pragma unroll
     for (int j = 0; j < J; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) to[(16 * j + 4 * quarter + i) * P + p] = S[j][i];
+      for (int i = 0; i < 2; ++i) {
+        const int n = 16 * j + 4 * quarter + 2 * i;
+        to[n * P + p] = S[j][i].x;
+        to[(n + 1) * P + p] = S[j][i].y;
+      }
   };
   const float A = a.A[h], skip = a.D ? a.D[h] : 0.f;
   float total = 0.f;  // sum of d (thread 0)
 
-  for (int t0 = it.begin; t0 < it.end; t0 += TB) {
-    const int nt = min(TB, it.end - t0);
+  // blocks of TB tokens that end at multiples of TB of the position, so snapshots fall on their ends
+  for (int t0 = it.begin, nt; t0 < it.end; t0 += nt) {
+    nt = min(TB - (it.s.ctx + t0) % TB, it.end - t0);
     const int64_t row0 = (int64_t)it.s.start + t0;
     __syncthreads();
     for (int e = tid; e < nt * N; e += NT) {
@@ -80,33 +88,31 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
     __syncthreads();
     if (!kOut && tid == 0)
       for (int t = 0; t < nt; ++t) total += sd[t];
+#pragma unroll 4
     for (int t = 0; t < nt; ++t) {
-      const float keep = sa[t], xv = sx[t][p], dx = sd[t] * xv;
-      float y = 0.f;
+      const float xv = sx[t][p], dx = sd[t] * xv;
+      const float2 keep2 = make_float2(sa[t], sa[t]), dx2 = make_float2(dx, dx);
+      float2 y0 = make_float2(0.f, 0.f), y1 = y0;
 #pragma unroll
       for (int j = 0; j < J; ++j) {
         const float4 b = *reinterpret_cast<const float4 *>(&sB[t][16 * j + 4 * quarter]);
-        S[j][0] = fmaf(b.x, dx, keep * S[j][0]);
-        S[j][1] = fmaf(b.y, dx, keep * S[j][1]);
-        S[j][2] = fmaf(b.z, dx, keep * S[j][2]);
-        S[j][3] = fmaf(b.w, dx, keep * S[j][3]);
+        S[j][0] = __ffma2_rn(make_float2(b.x, b.y), dx2, __fmul2_rn(keep2, S[j][0]));
+        S[j][1] = __ffma2_rn(make_float2(b.z, b.w), dx2, __fmul2_rn(keep2, S[j][1]));
         if (kOut) {
           const float4 c = *reinterpret_cast<const float4 *>(&sC[t][16 * j + 4 * quarter]);
-          y = fmaf(c.x, S[j][0], y);
-          y = fmaf(c.y, S[j][1], y);
-          y = fmaf(c.z, S[j][2], y);
-          y = fmaf(c.w, S[j][3], y);
+          y0 = __ffma2_rn(make_float2(c.x, c.y), S[j][0], y0);
+          y1 = __ffma2_rn(make_float2(c.z, c.w), S[j][1], y1);
         }
       }
       if (kOut) {
+        float y = (y0.x + y0.y) + (y1.x + y1.y);
         y += __shfl_xor_sync(~0u, y, 1);
         y += __shfl_xor_sync(~0u, y, 2);
         if (quarter == 0) sy[t][p] = fmaf(skip, xv, y);
-        if (a.page)
-          if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(t0 + t + 1), tell)) save(to);
       }
     }
     if (kOut) {
+      if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(t0 + nt), tell)) save(to);
       __syncthreads();
       for (int e = tid; e < nt * P; e += NT) {
         const int t = e / P, c = e % P;
@@ -168,9 +174,10 @@ __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a,
 //   resident : blocks that run at once
 //   state_cost : time of a state pass over a chunk, in output passes
 //   launch_cost : time of the two more launches, in tokens of the output pass
+//   shortest : tokens that a segment has at least
 // Whole sequences run as long as the longest of them; packed ones (whose lengths
 // the host does not see) are taken to hold one of twice the mean.
-int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int launch_cost, bool packed) {
+int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int launch_cost, int shortest, bool packed) {
   auto waves = [&](double items) { return ceil(items * blocks / resident); };
   const double mean = (double)rows / R;
   const double most = packed && R > 1 ? fmin((double)rows, 2 * mean) : mean;
@@ -179,7 +186,7 @@ int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost
   int seg = 0;
   for (int k = 2; k <= 64; ++k) {
     const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
-    if (len < 4 * kAlign) break;
+    if (len < shortest) break;
     const double items = packed && R > 1 ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
     const double cost = waves(items) * len * (1 + state_cost) + launch_cost;
     if (cost < best) {
@@ -192,11 +199,11 @@ int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost
 
 // The CUDA-core kernel: two blocks of 512 threads share an SM; a token takes about
 // 0.2 us, its state pass saves the outputs' half.
-int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 64, packed); }
+int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 64, kAlign, packed); }
 // The tensor-core kernel: one block an SM; a chunk takes 2.6 us, 1.1 us in the state
 // pass; the two launches about 10 us.
 int tc_segment(int R, int rows, int H, int P, bool packed) {
-  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.43f, 4 * kAlign, packed);
+  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.43f, 4 * kAlign, 4 * kAlign, packed);
 }
 
 template <int N, int P, typename T>

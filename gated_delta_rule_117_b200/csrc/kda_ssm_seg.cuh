@@ -22,7 +22,7 @@ inline int64_t scan_items(int R, int rows, int seg) { return seg == 0 ? R : (int
 
 __device__ __forceinline__ int seg_base(const Requests &q, int r, int seg) {
   if (seg == 0) return r;
-  const int start = q.cu ? q.cu[r] : r * (q.rows / q.R);
+  const int start = q.cu ? q.cu[r] : r * q.T;
   return start / seg + 2 * r;
 }
 
