@@ -128,27 +128,28 @@ struct Misc {
   uint64_t wait_ns;
 };
 
-// One copy of the wait for every role: the roles' hot loops together should fit
-// the SM's instruction cache (unrolled and inlined to 108 KB, the kernel spent a
-// third of its time waiting for instructions, and more on the SMs that share a
-// larger cache level with others).  The whole warp calls it and gets the same
+// The sleeping part of a wait, one copy for every role (the roles' hot loops together
+// should fit the SM's instruction cache: unrolled and inlined to 108 KB, the kernel
+// spent a third of its time waiting for instructions, and more on the SMs that share
+// a larger cache level with others).  The whole warp calls it and gets the same
 // answer, as warp-wide instructions follow.
-__device__ __noinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *m) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (__all_sync(~0u, ok)) return true;
-  if (!ok) {
-    const uint64_t t0 = global_ns();
-    for (;;) {
-      if ((ok = mbar_try_wait_sleep(bar, parity, 1000000u))) break;
-      if (m->abort) break;
-      if (global_ns() - t0 > m->wait_ns) {
-        m->abort = 1;
-        atomicExch(m->status, kDevTimeout);
-        break;
-      }
+__device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Misc *m) {
+  bool ok = false;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    if ((ok = mbar_try_wait_sleep(bar, parity, 1000000u))) break;
+    if (m->abort) break;
+    if (global_ns() - t0 > m->wait_ns) {
+      m->abort = 1;
+      atomicExch(m->status, kDevTimeout);
+      break;
     }
   }
   return __all_sync(~0u, ok);
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *m) {
+  return __all_sync(~0u, mbar_try_wait(bar, parity)) || wait_slow(bar, parity, m);
 }
 
 struct Cta {
@@ -281,27 +282,36 @@ __global__ void __launch_bounds__(NT, 1)
     for (int i = 0; i < n; ++i) {
       const int st = i & 1, row = row_of_seq + ch.first(i);
       if (i >= 2 && !(ok = x.wait2(BX_FREE, i - 2))) break;
-      mbar_arrive_expect_tx_warp(&x.bar[F_BX + st], half + 16384u);
-      tma_load_3d_warp(sm + kX + st * 16384, &mx, &x.bar[F_BX + st], p0, h, row);
-#pragma unroll 1
-      for (int c = 0; c < 16 * NK; c += 64)
-        tma_load_3d_warp(sm + kB + st * 32768 + c * 256, &mb, &x.bar[F_BX + st], c, g, row);
+      if (elect_one()) {
+        mbar_arrive_expect_tx(&x.bar[F_BX + st], half + 16384u);
+        tma_load_3d(sm + kX + st * 16384, &mx, &x.bar[F_BX + st], p0, h, row);
+#pragma unroll
+        for (int c = 0; c < 16 * NK; c += 64)
+          tma_load_3d(sm + kB + st * 32768 + c * 256, &mb, &x.bar[F_BX + st], c, g, row);
+      }
+      __syncwarp();
       loads = i + 1;
       if (kOut) {
         if (i >= 1 && !(ok = x.wait(C_FREE, i - 1))) break;
-        mbar_arrive_expect_tx_warp(&x.bar[F_C], half);
-#pragma unroll 1
-        for (int c = 0; c < 16 * NK; c += 64) tma_load_3d_warp(sm + kC + c * 256, &mc, &x.bar[F_C], c, g, row);
+        if (elect_one()) {
+          mbar_arrive_expect_tx(&x.bar[F_C], half);
+#pragma unroll
+          for (int c = 0; c < 16 * NK; c += 64) tma_load_3d(sm + kC + c * 256, &mc, &x.bar[F_C], c, g, row);
+        }
+        __syncwarp();
         cloads = i + 1;
       }
       if (i + 2 < n) {  // the chunk after the next on its way from HBM
         const int next = row_of_seq + ch.first(i + 2);
-        tma_prefetch_3d_warp(&mx, p0, h, next);
-#pragma unroll 1
-        for (int c = 0; c < 16 * NK; c += 64) {
-          tma_prefetch_3d_warp(&mb, c, g, next);
-          if (kOut) tma_prefetch_3d_warp(&mc, c, g, next);
+        if (elect_one()) {
+          tma_prefetch_3d(&mx, p0, h, next);
+#pragma unroll
+          for (int c = 0; c < 16 * NK; c += 64) {
+            tma_prefetch_3d(&mb, c, g, next);
+            if (kOut) tma_prefetch_3d(&mc, c, g, next);
+          }
         }
+        __syncwarp();
       }
     }
     if (!ok) {  // loads in flight must land before shared memory is given up
@@ -322,10 +332,6 @@ __global__ void __launch_bounds__(NT, 1)
     const uint64_t dS = sdesc_sw128(sbase + kS, 16, 1024);
     const uint64_t dW = sdesc_sw128(sbase + kW, 16384, 1024);
     const uint64_t dC = sdesc_sw128(sbase + kC, 16, 1024);
-    // a wait of this warp, whose every instruction delays the tensor core: tried in line
-    auto ready = [&](int b, int k) {
-      return __all_sync(~0u, mbar_try_wait(&x.bar[b], k & 1)) || x.wait(b, k);
-    };
     // byte offset of K step k in a [128 x 128] tile, K along its rows
     auto koff = [](int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32); };
 #pragma unroll 1
@@ -334,10 +340,10 @@ __global__ void __launch_bounds__(NT, 1)
       const uint64_t dB = sdesc_sw128(sbase + kB + st * 32768, 16, 1024);
       const uint64_t dBt = sdesc_sw128(sbase + kB + st * 32768, 16384, 1024);
       const uint64_t dX = sdesc_sw128(sbase + kX + st * 16384, 16, 1024);
-      if (!ready(F_BX + st, i >> 1)) break;
+      if (!x.wait2(F_BX, i)) break;
       if (kOut) {
         // (the G before was read before its W was ready)
-        if (!ready(F_C, i)) break;
+        if (!x.wait(F_C, i)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -345,7 +351,7 @@ __global__ void __launch_bounds__(NT, 1)
           mma_commit(&x.bar[G_DONE]);
         }
         __syncwarp();
-        if (!ready(YX_READY, i)) break;
+        if (!x.wait(YX_READY, i)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -354,7 +360,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncwarp();
       }
-      if (!ready(WX_READY, i)) break;
+      if (!x.wait(WX_READY, i)) break;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
@@ -364,7 +370,7 @@ __global__ void __launch_bounds__(NT, 1)
       }
       __syncwarp();
       if (kOut) {
-        if (!ready(W_READY, i)) break;
+        if (!x.wait(W_READY, i)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -417,19 +423,21 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_ld16(tg + 32 * (c + 1), v);
         tmem_st8(tw + 16 * c, w);
       }
-      float e[16];  // the diagonal block's factors, formed while its scores arrive
+      float2 e[8];  // the diagonal block's factors, formed while its scores arrive
 #pragma unroll
-      for (int j = 0; j < 16; j += 4) {
-        const float4 f = f4(D.pre + 32 * b + 16 * half + j), d = f4(D.d + 32 * b + 16 * half + j);
-        e[j] = d.x * ex2(pre - f.x);
-        e[j + 1] = d.y * ex2(pre - f.y);
-        e[j + 2] = d.z * ex2(pre - f.z);
-        e[j + 3] = d.w * ex2(pre - f.w);
+      for (int j = 0; j < 8; j += 2) {
+        const float4 f = f4(D.pre + 32 * b + 16 * half + 2 * j), d = f4(D.d + 32 * b + 16 * half + 2 * j);
+        e[j] = __fmul2_rn(make_float2(d.x, d.y), make_float2(ex2(pre - f.x), ex2(pre - f.y)));
+        e[j + 1] = __fmul2_rn(make_float2(d.z, d.w), make_float2(ex2(pre - f.z), ex2(pre - f.w)));
       }
       tmem_ld_wait(v);
 #pragma unroll
-      for (int j = 0; j < 16; j += 2)
-        w[j / 2] = pack_bf16x2(16 * half + j <= lane ? v[j] * e[j] : 0.f, 16 * half + j + 1 <= lane ? v[j + 1] * e[j + 1] : 0.f);
+      for (int j = 0; j < 8; ++j) {
+        const float2 r = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), e[j]);
+        // columns behind the row: zeros, whatever the scores and factors are
+        const int behind = 16 * half + 2 * j - lane;
+        w[j] = pack_bf16x2(r.x, r.y) & (behind < 0 ? ~0u : behind == 0 ? 0xffffu : 0u);
+      }
       tmem_st8(tw + 16 * b, w);
       tmem_st_wait();
       tc_fence_before();
@@ -561,26 +569,25 @@ __global__ void __launch_bounds__(NT, 1)
     const int half = (warp - 16) >> 2;
     const int cols = t < a.N ? min(32, a.P - p0 - 32 * half) : 0;  // columns that exist
     const int64_t np = (int64_t)a.N * a.P, at = (int64_t)t * a.P + p0 + 32 * half;
-    float S[32];
+    float2 S[16];
     const float *from = nullptr;
     if (kOut) {
       if (p.seg != 0) from = p.ws + (it.item * a.H + h) * np + at;
       else if (a.state && it.s.ctx > 0) from = a.state + ((int64_t)it.s.slot * a.H + h) * np + at;
     }
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 v = from && j < cols ? f4(from + j) : make_float4(0.f, 0.f, 0.f, 0.f);
-      S[j] = v.x; S[j + 1] = v.y; S[j + 2] = v.z; S[j + 3] = v.w;
+    for (int j = 0; j < 16; j += 2) {
+      const float4 v = from && 2 * j < cols ? f4(from + 2 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
+      S[j] = make_float2(v.x, v.y);
+      S[j + 1] = make_float2(v.z, v.w);
     }
     auto copy = [&]() {  // the bf16 copy that the next chunk's outputs read
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        uint4 v;
-        v.x = pack_bf16x2(S[8 * k + 0], S[8 * k + 1]);
-        v.y = pack_bf16x2(S[8 * k + 2], S[8 * k + 3]);
-        v.z = pack_bf16x2(S[8 * k + 4], S[8 * k + 5]);
-        v.w = pack_bf16x2(S[8 * k + 6], S[8 * k + 7]);
-        *reinterpret_cast<uint4 *>(sm + kS + sw128_chunk(t, 4 * half + k)) = v;
+        uint32_t v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = pack_bf16x2(S[4 * k + j].x, S[4 * k + j].y);
+        *reinterpret_cast<uint4 *>(sm + kS + sw128_chunk(t, 4 * half + k)) = make_uint4(v[0], v[1], v[2], v[3]);
       }
       fence_proxy_async_smem();
       x.arrive(YX_READY);
@@ -604,7 +611,11 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_ld_touch(q1);
         tmem_ld_touch(q2);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) S[c + j] = fmaf(keep, S[c + j], q0[j] + (q1[j] + q2[j]));
+        for (int j = 0; j < 4; ++j) {
+          const float2 low = __fadd2_rn(make_float2(q1[2 * j], q1[2 * j + 1]), make_float2(q2[2 * j], q2[2 * j + 1]));
+          const float2 sum = __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), low);
+          S[c / 2 + j] = __ffma2_rn(make_float2(keep, keep), S[c / 2 + j], sum);
+        }
       }
       tc_fence_before();
       x.arrive(WX_READY);
@@ -620,8 +631,8 @@ __global__ void __launch_bounds__(NT, 1)
       for (int k = 0; k < 2; ++k, to = last) {
         if (!to) continue;
 #pragma unroll
-        for (int j = 0; j < 32; j += 4)
-          if (j < cols) *reinterpret_cast<float4 *>(to + at + j) = make_float4(S[j], S[j + 1], S[j + 2], S[j + 3]);
+        for (int j = 0; j < 16; j += 2)
+          if (2 * j < cols) *reinterpret_cast<float4 *>(to + at + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
       }
     }
   } else if (kOut && warp >= 24) {

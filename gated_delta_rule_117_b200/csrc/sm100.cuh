@@ -305,13 +305,10 @@ __device__ __forceinline__ void tma_load_3d_warp(void *smem_dst, const CUtensorM
       : "memory");
 }
 // Brings a tile into L2 (no completion to wait for).
-__device__ __forceinline__ void tma_prefetch_3d_warp(const CUtensorMap *map, int c0, int c1, int c2) {
-  asm volatile(
-      "{\n\t.reg .pred e;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];\n\t}" ::"l"(reinterpret_cast<uint64_t>(map)),
-      "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap *map, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
 }
 // TMA tiled store shared -> global (bulk-group completion), issued by one
 // elected lane of a converged warp; commit and read-completion wait likewise.
