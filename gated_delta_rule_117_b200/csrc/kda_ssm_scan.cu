@@ -36,7 +36,8 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
   const int h = blockIdx.x % a.H;
   const bool tell = kOut && h == 0 && tid == 0;
   Item it;
-  if (!item_of(a.q, blockIdx.x / a.H, seg, tell, it)) return;
+  __shared__ int scratch[kMaxRanked + 1];
+  if (!item_of(a.q, blockIdx.x / a.H, seg, tell, scratch, it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const int g = h / (a.H / a.G);
   float2 S[J][2];  // rows 16 j + 4 quarter + 0 .. 3
@@ -173,22 +174,24 @@ __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a,
 //   blocks : blocks that an item of `H` heads makes
 //   resident : blocks that run at once
 //   state_cost : time of a state pass over a chunk, in output passes
+//   block_cost : time that a block takes to begin and to end, in tokens
 //   launch_cost : time of the two more launches, in tokens of the output pass
 //   shortest : tokens that a segment has at least
 // Whole sequences run as long as the longest of them; packed ones (whose lengths
 // the host does not see) are taken to hold one of twice the mean.
-int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int launch_cost, int shortest, bool packed) {
+int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int block_cost, int launch_cost, int shortest,
+                 bool packed) {
   auto waves = [&](double items) { return ceil(items * blocks / resident); };
   const double mean = (double)rows / R;
   const double most = packed && R > 1 ? fmin((double)rows, 2 * mean) : mean;
   // blocks of unequal length fill the machine as they come: the waves' total, or the longest block
-  double best = packed && R > 1 ? fmax(most, mean * R * blocks / resident) : waves(R) * mean;
+  double best = packed && R > 1 ? fmax(most, (mean + block_cost) * R * blocks / resident) : waves(R) * (mean + block_cost);
   int seg = 0;
   for (int k = 2; k <= 64; ++k) {
     const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
     if (len < shortest) break;
     const double items = packed && R > 1 ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
-    const double cost = waves(items) * len * (1 + state_cost) + launch_cost;
+    const double cost = waves(items) * (len + block_cost) * (1 + state_cost) + launch_cost;
     if (cost < best) {
       best = cost;
       seg = len;
@@ -199,11 +202,12 @@ int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost
 
 // The CUDA-core kernel: two blocks of 512 threads share an SM; a token takes about
 // 0.2 us, its state pass saves the outputs' half.
-int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 64, kAlign, packed); }
-// The tensor-core kernel: one block an SM; a chunk takes 2.6 us, 1.1 us in the state
-// pass; the two launches about 10 us.
+int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 16, 64, kAlign, packed); }
+// The tensor-core kernel: one block an SM; a chunk takes 2.3 us, 1.0 us in the state
+// pass; a block's beginning and end 6 us, the two launches about 10 us.
 int tc_segment(int R, int rows, int H, int P, bool packed) {
-  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.43f, 4 * kAlign, 4 * kAlign, packed);
+  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.43f, 5 * kAlign / 2, 4 * kAlign,
+                      4 * kAlign, packed);
 }
 
 template <int N, int P, typename T>

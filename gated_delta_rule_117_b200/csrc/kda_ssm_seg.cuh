@@ -34,10 +34,33 @@ struct Item {
   int64_t item;        // its number (workspace entry)
 };
 
-// The block's work item; false: none.  Every thread of the block must call it.
-__device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, bool tell, Item &it) {
+// Requests of a packed call up to which whole sequences run longest first.
+constexpr int kMaxRanked = 1024;
+
+// Sequence of rank `item` by length, longest first (ties: lower index first), so that the
+// longest do not begin when the machine is already running dry: 9 sequences of 362 to
+// 7,305 tokens, 32 heads: 254 us in the order of the call, 185 us longest first.
+// `scratch`: kMaxRanked + 1 ints of shared memory.  Every thread of the block calls it.
+__device__ __forceinline__ int sequence_of_rank(const Requests &q, int item, int *scratch) {
+  for (int r = threadIdx.x; r < q.R; r += blockDim.x) scratch[r] = q.cu[r + 1] - q.cu[r];
+  __syncthreads();
+  for (int r = threadIdx.x; r < q.R; r += blockDim.x) {
+    const int len = scratch[r];
+    int rank = 0;
+    for (int k = 0; k < q.R; ++k) rank += scratch[k] > len || (scratch[k] == len && k < r);
+    if (rank == item) scratch[kMaxRanked] = r;
+  }
+  __syncthreads();
+  const int r = scratch[kMaxRanked];
+  __syncthreads();
+  return r;
+}
+
+// The block's work item; false: none.  Every thread of the block must call it;
+// `scratch` as above.
+__device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, bool tell, int *scratch, Item &it) {
   if (seg == 0) {
-    it.r = item;
+    it.r = q.cu && q.R > 1 && q.R <= kMaxRanked ? sequence_of_rank(q, item, scratch) : item;
   } else {
     it.r = block_count_le(q.R, [&](int i) { return seg_base(q, i, seg); }, item) - 1;
     if (it.r < 0) return false;
@@ -47,7 +70,7 @@ __device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, bo
   const int len = it.s.end - it.s.start;
   if (!it.s.ok || len == 0) return false;
   const int off = it.s.ctx % kAlign;
-  it.index = item - seg_base(q, it.r, seg);
+  it.index = seg == 0 ? 0 : item - seg_base(q, it.r, seg);
   it.count = seg == 0 ? 1 : (int)(((int64_t)off + len + seg - 1) / seg);
   if (it.index < 0 || it.index >= it.count) return false;
   it.begin = it.index == 0 ? 0 : it.index * seg - off;

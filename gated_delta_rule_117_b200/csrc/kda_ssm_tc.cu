@@ -232,14 +232,14 @@ __global__ void __launch_bounds__(NT, 1)
   const int slices = (a.P + PC - 1) / PC;
   const int p0 = (int)(blockIdx.x % slices) * PC, h = (int)(blockIdx.x / slices % a.H);
   const bool tell = kOut && p0 == 0 && h == 0 && tid == 0;
+  unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   Item it;
-  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, it)) return;
+  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, reinterpret_cast<int *>(sm + kW), it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const Chunks ch(it);
   const int n = ch.n, g = h / (a.H / a.G);
 
   Cta x;
-  unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   x.sm = sm;
   x.bar = reinterpret_cast<uint64_t *>(sm + kBarOff);
   x.m = reinterpret_cast<Misc *>(sm + kMisc);
@@ -343,19 +343,16 @@ __global__ void __launch_bounds__(NT, 1)
       if (!x.wait2(F_BX, i)) break;
       if (kOut) {
         // (the G before was read before its W was ready)
-        if (!x.wait(F_C, i)) break;
-        tc_fence_after();
-        if (elect_one()) {
-#pragma unroll
-          for (int k = 0; k < NK; ++k) mma_bf16(tb + tG, sdesc_add(dC, koff(k)), sdesc_add(dB, koff(k)), idG, k > 0);
-          mma_commit(&x.bar[G_DONE]);
-        }
-        __syncwarp();
-        if (!x.wait(YX_READY, i)) break;
+        // Yx first: it waits longest for what it reads, and C is free for the next chunk once both
+        // are done (G first: 2.44 us a chunk against 2.36)
+        if (!x.wait(F_C, i) || !x.wait(YX_READY, i)) break;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
           for (int k = 0; k < NK; ++k) mma_bf16(tb + tYx, sdesc_add(dC, koff(k)), sdesc_add(dS, k * 2048), idYx, k > 0);
+#pragma unroll
+          for (int k = 0; k < NK; ++k) mma_bf16(tb + tG, sdesc_add(dC, koff(k)), sdesc_add(dB, koff(k)), idG, k > 0);
+          mma_commit(&x.bar[G_DONE]);
           mma_commit(&x.bar[C_FREE]);
         }
         __syncwarp();
