@@ -565,13 +565,20 @@ __global__ void __launch_bounds__(NT, 1)
     // ======================= state =======================
     const int half = (warp - 16) >> 2;
     const int cols = t < a.N ? min(32, a.P - p0 - 32 * half) : 0;  // columns that exist
-    const int64_t np = (int64_t)a.N * a.P, at = (int64_t)t * a.P + p0 + 32 * half;
+    const int at = t * a.P + p0 + 32 * half;
     float2 S[16];
     const float *from = nullptr;
     if (kOut) {
+      const int64_t np = (int64_t)a.N * a.P;
       if (p.seg != 0) from = p.ws + (it.item * a.H + h) * np + at;
       else if (a.state && it.s.ctx > 0) from = a.state + ((int64_t)it.s.slot * a.H + h) * np + at;
     }
+    auto save = [&](float *to) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 2)
+        if (2 * j < cols) *reinterpret_cast<float4 *>(to + at + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
+    };
+    bool done = false;
 #pragma unroll
     for (int j = 0; j < 16; j += 2) {
       const float4 v = from && 2 * j < cols ? f4(from + 2 * j) : make_float4(0.f, 0.f, 0.f, 0.f);
@@ -600,37 +607,33 @@ __global__ void __launch_bounds__(NT, 1)
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
-        float q0[8], q1[8], q2[8];
-        tmem_ld8(tl + tDS + 32 * half + c, q0);
+        float q0[8], q1[8];
+        tmem_ld8(tl + tDS + 128 + 32 * half + c, q0);
         tmem_ld8(tl + tDS + 64 + 32 * half + c, q1);
-        tmem_ld8(tl + tDS + 128 + 32 * half + c, q2);
         tmem_ld_wait(q0);
         tmem_ld_touch(q1);
-        tmem_ld_touch(q2);
+        float2 sum[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 low = __fadd2_rn(make_float2(q1[2 * j], q1[2 * j + 1]), make_float2(q2[2 * j], q2[2 * j + 1]));
-          const float2 sum = __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), low);
-          S[c / 2 + j] = __ffma2_rn(make_float2(keep, keep), S[c / 2 + j], sum);
-        }
+        for (int j = 0; j < 4; ++j)
+          sum[j] = __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), make_float2(q1[2 * j], q1[2 * j + 1]));
+        tmem_ld8(tl + tDS + 32 * half + c, q0);
+        tmem_ld_wait(q0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          S[c / 2 + j] = __ffma2_rn(make_float2(keep, keep), S[c / 2 + j], __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), sum[j]));
       }
       tc_fence_before();
       x.arrive(WX_READY);
       if (kOut && i + 1 < n) copy();  // (DS_DONE: the products that read the copy before are done)
-      // after the chunk: a snapshot, and after the last one the state's own place
-      float *to = nullptr, *last = nullptr;
-      if (kOut && a.page) to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(ch.first(i) + ch.count(i)), p0 == 0 && t == 0);
-      if (i == n - 1) {
-        if (!kOut) last = p.ws + (it.item * a.H + h) * np;
-        else if (a.state && it.index == it.count - 1) last = a.state + ((int64_t)it.s.slot * a.H + h) * np;
+      if (kOut && a.page) {
+        if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(ch.first(i) + ch.count(i)), p0 == 0 && t == 0))
+          save(to);
       }
-#pragma unroll 1
-      for (int k = 0; k < 2; ++k, to = last) {
-        if (!to) continue;
-#pragma unroll
-        for (int j = 0; j < 16; j += 2)
-          if (2 * j < cols) *reinterpret_cast<float4 *>(to + at + 2 * j) = make_float4(S[j].x, S[j].y, S[j + 1].x, S[j + 1].y);
-      }
+      done = i + 1 == n;
+    }
+    if (done) {
+      if (!kOut) save(p.ws + (it.item * a.H + h) * ((int64_t)a.N * a.P));
+      else if (a.state && it.index == it.count - 1) save(a.state + ((int64_t)it.s.slot * a.H + h) * ((int64_t)a.N * a.P));
     }
   } else if (kOut && warp >= 24) {
     // ======================= outputs =======================
