@@ -97,18 +97,21 @@ __device__ __forceinline__ Seq seq_of(const Requests &q, int r, bool tell) {
   return s;
 }
 
-// Number of entries i in [0, n) with key(i) <= v, key non-decreasing, counted by
-// the whole block (every thread gets it; holds barriers).
+// Number of entries i in [0, n) with key(i) <= v, key non-decreasing, found by the
+// whole block (every thread gets it; holds barriers): each step samples one entry a
+// thread and keeps the gap between two samples.
 template <typename F>
 __device__ __forceinline__ int block_count_le(int n, F key, int v) {
-  int c = 0;
-  for (int i0 = 0; i0 < n; i0 += blockDim.x) {
-    const int i = i0 + threadIdx.x;
-    const int here = __syncthreads_count(i < n && key(i) <= v);
-    c += here;
-    if (here < (int)blockDim.x) break;  // the keys do not decrease
+  int lo = 0, hi = n;  // the count lies in [lo, hi]
+  while (lo < hi) {
+    const int step = (hi - lo + blockDim.x - 1) / blockDim.x;
+    const int64_t i = lo + (int64_t)threadIdx.x * step;
+    const int c = __syncthreads_count(i < hi && key((int)i) <= v);
+    if (c == 0) return lo;
+    hi = (int)min((int64_t)hi, lo + (int64_t)c * step);
+    lo += (c - 1) * step + 1;
   }
-  return c;
+  return lo;
 }
 
 __device__ __forceinline__ float as_float(float x) { return x; }

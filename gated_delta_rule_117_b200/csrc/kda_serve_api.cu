@@ -11,6 +11,7 @@ namespace {
 using namespace kda::check;
 
 constexpr int kMaxMapRequests = 16384;
+constexpr int kMaxChannels = 1 << 24;  // a block for each 512 of them in a grid's second dimension
 
 size_t elem(kda_dtype_t t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
 
@@ -48,7 +49,7 @@ kda_status_t check_conv(const void *x, int64_t x_stride, const void *w, const vo
                         int64_t y_stride, int C, int K, int head_dim, kda_dtype_t dtype, int flags, float eps) {
   if (C < 0) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_DTYPE;
-  if (K < 2 || K > 4) return KDA_ERR_SHAPE;
+  if (K < 2 || K > 4 || C > kMaxChannels) return KDA_ERR_SHAPE;
   if (flags & ~(KDA_CONV_SILU | KDA_CONV_L2NORM | KDA_CONV_HEAD_MAJOR)) return KDA_ERR_INVALID_ARG;
   const bool heads = (flags & (KDA_CONV_L2NORM | KDA_CONV_HEAD_MAJOR)) != 0;
   if (heads && (!supported_d(head_dim) || C % head_dim != 0)) return KDA_ERR_SHAPE;

@@ -352,8 +352,8 @@ size_t kda_noalloc_scratch_bytes(void);
  *   R, rows  : sequences, and rows of the token-major arrays
  *   cu       : [R + 1] int32, non-decreasing; sequence r owns rows cu[r] ..
  *              cu[r + 1] - 1 (none is allowed), and cu[R] <= rows.  Rows before
- *              cu[0] and from cu[R] on belong to no sequence and are neither
- *              read nor written.  NULL: R sequences of rows / R tokens each
+ *              cu[0] and from cu[R] on belong to no sequence: what they hold
+ *              does not matter, and they are not written.  NULL: R sequences of rows / R tokens each
  *              (rows % R == 0, else KDA_ERR_SHAPE).
  *   ctx      : [R] int32, tokens that each sequence has behind it already; a
  *              sequence with ctx[r] <= 0 starts from a zero state, others from
@@ -431,7 +431,7 @@ enum {
  *   head_dim: one of 16, 32, 64, 128 dividing C with KDA_CONV_L2NORM or
  *             KDA_CONV_HEAD_MAJOR; ignored otherwise
  *   eps     : of the norm; finite, >= 0
- *   K       : 2, 3 or 4 taps
+ *   K       : 2, 3 or 4 taps;   C : at most 2^24
  * Sums are fp32 and rounded once.
  */
 kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *w, const void *bias, void *state, int n_slots,
