@@ -21,7 +21,9 @@ namespace kda {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kBlocks = 6;  // an SM: 80 registers (7 and 8 spill: 225 and 253 us against 216 at 65,536 x 4,352 bf16)
+// Blocks an SM: 6 leave 80 registers (7 and 8 spill: 225 and 253 us against 216 at 65,536 x
+// 4,352 bf16), 5 leave the norm of four rows at a time its 96.
+constexpr int blocks_of(bool norm) { return norm ? 5 : 6; }
 constexpr int V = 4;  // channels of a thread
 
 // Four elements as loaded.
@@ -171,9 +173,7 @@ struct Queue {
   }
 };
 
-// Output of one row from its K inputs, oldest first.  A head's channels lie in
-// d / V neighbouring lanes, so its norm is a butterfly over them: every lane of
-// the warp must come here.
+// The convolution and Swish of one row from its K inputs, oldest first.
 template <typename T, int K>
 __device__ __forceinline__ F4 conv_row(const ConvArgs &a, const Taps<K> &t, const F4 (&u)[K]) {
   F4 o = t.b;
@@ -186,19 +186,33 @@ __device__ __forceinline__ F4 conv_row(const ConvArgs &a, const Taps<K> &t, cons
     o.a = swish(o.a, T());
     o.b = swish(o.b, T());
   }
-  if (a.norm) {
-    float2 q = __ffma2_rn(o.a, o.a, __fmul2_rn(o.b, o.b));
-    float ss = q.x + q.y;
-    for (int off = 1; off < a.d / V; off <<= 1) ss += __shfl_xor_sync(~0u, ss, off);
-    const float f = inverse_root(ss + a.eps, T());
-    o.a = __fmul2_rn(o.a, make_float2(f, f));
-    o.b = __fmul2_rn(o.b, make_float2(f, f));
-  }
   return o;
 }
 
-template <typename T, int K, bool VEC>
-__global__ void __launch_bounds__(kThreads, kBlocks) short_conv_kernel(ConvArgs a, int tile) {
+// The L2 norm of NR rows' heads.  A head's channels lie in d / V neighbouring lanes, so
+// its sum is a butterfly over them, the rows' in step: every lane of the warp must come
+// here.
+template <typename T, int NR>
+__device__ __forceinline__ void norm_rows(const ConvArgs &a, F4 (&o)[NR]) {
+  float ss[NR];
+#pragma unroll
+  for (int b = 0; b < NR; ++b) {
+    const float2 q = __ffma2_rn(o[b].a, o[b].a, __fmul2_rn(o[b].b, o[b].b));
+    ss[b] = q.x + q.y;
+  }
+  for (int off = 1; off < a.d / V; off <<= 1)
+#pragma unroll
+    for (int b = 0; b < NR; ++b) ss[b] += __shfl_xor_sync(~0u, ss[b], off);
+#pragma unroll
+  for (int b = 0; b < NR; ++b) {
+    const float f = inverse_root(ss[b] + a.eps, T());
+    o[b].a = __fmul2_rn(o[b].a, make_float2(f, f));
+    o[b].b = __fmul2_rn(o[b].b, make_float2(f, f));
+  }
+}
+
+template <typename T, int K, bool VEC, bool NORM>
+__global__ void __launch_bounds__(kThreads, blocks_of(NORM)) short_conv_kernel(ConvArgs a, int tile) {
   __shared__ Raw<T> rows_ahead[VEC ? kDepth * kThreads : 1];
   Queue<T> queue;
   queue.mine = rows_ahead + (VEC ? threadIdx.x : 0);
@@ -280,32 +294,47 @@ __global__ void __launch_bounds__(kThreads, kBlocks) short_conv_kernel(ConvArgs 
           const int p = at - (K - 1) + i - s.start;
           u[i] = widen(load4<T, VEC>(p >= 0 ? x + (s.start + p) * xs : entry + (int64_t)(p + K - 1) * a.C, n));
         }
-        store4<T, VEC>(y + (at - s.start) * ys, n, conv_row<T, K>(a, taps, u));
+        F4 o[1] = {conv_row<T, K>(a, taps, u)};
+        if (NORM) norm_rows<T>(a, o);
+        store4<T, VEC>(y + (at - s.start) * ys, n, o[0]);
       }
     }
     const int first = carry && !here ? s.start + K - 1 : row;  // rows before it are another tile's
     T *yr = y + (row - s.start) * ys;
-    // one row: its inputs are h and `in`, which then moves into h
-    auto step = [&](const Raw<T> &in, T *to, bool keep) {
+    // one row before its norm: its inputs are h and `in`, which then moves into h
+    auto step = [&](const Raw<T> &in) {
       F4 w[K];
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) w[i] = h[i];
       w[K - 1] = widen(in);
-      const F4 o = conv_row<T, K>(a, taps, w);
-      if (keep) store4<T, VEC>(to, n, o);
 #pragma unroll
       for (int i = 0; i < K - 1; ++i) h[i] = w[i + 1];
+      return conv_row<T, K>(a, taps, w);
     };
     while (row < stop) {
       if (VEC && queue.i == 0 && row + kGroup <= stop && row >= first) {  // a whole group
         queue.wait();
+        F4 o[kGroup];
 #pragma unroll
-        for (int b = 0; b < kGroup; ++b, yr += ys) step(queue.row(b), yr, true);
-        row += kGroup;
+        for (int b = 0; b < kGroup; ++b) {
+          o[b] = step(queue.row(b));
+          if (!NORM) {
+            store4<T, VEC>(yr, n, o[b]);
+            yr += ys;
+          }
+        }
         queue.next_group();
+        if (NORM) {
+          norm_rows<T>(a, o);
+#pragma unroll
+          for (int b = 0; b < kGroup; ++b, yr += ys) store4<T, VEC>(yr, n, o[b]);
+        }
+        row += kGroup;
       } else if constexpr (VEC) {
         if (queue.i == 0) queue.wait();
-        step(queue.row(queue.i), yr, row >= first);
+        F4 o[1] = {step(queue.row(queue.i))};
+        if (NORM) norm_rows<T>(a, o);
+        if (row >= first) store4<T, VEC>(yr, n, o[0]);
         if (++queue.i == kGroup) queue.next_group();
         ++row;
         yr += ys;
@@ -315,7 +344,11 @@ __global__ void __launch_bounds__(kThreads, kBlocks) short_conv_kernel(ConvArgs 
         for (int b = 0; b < kGroup; ++b) in[b] = load4<T, VEC>(x + (row + b) * xs, row + b < stop ? n : 0);
 #pragma unroll
         for (int b = 0; b < kGroup; ++b)
-          if (row + b < stop) step(in[b], yr + b * ys, row + b >= first);
+          if (row + b < stop) {
+            F4 o[1] = {step(in[b])};
+            if (NORM) norm_rows<T>(a, o);
+            if (row + b >= first) store4<T, VEC>(yr + b * ys, n, o[0]);
+          }
         row += kGroup;
         yr += kGroup * ys;
       }
@@ -329,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, kBlocks) short_conv_kernel(ConvArgs 
   }
 }
 
-template <typename T, int K, bool VEC>
+template <typename T, int K, bool VEC, bool NORM>
 __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(ConvArgs a) {
   const int r = blockIdx.x;
   const int c0 = (blockIdx.y * kThreads + threadIdx.x) * V;
@@ -346,16 +379,20 @@ __global__ void __launch_bounds__(kThreads) short_conv_step_kernel(ConvArgs a) {
   for (int i = 0; i < K - 1; ++i) u[i] = widen(load4<T, VEC>(entry + (int64_t)i * a.C, n));
   u[K - 1] = widen(load4<T, VEC>((const T *)a.x + r * a.x_stride + c0, n));
   const Taps<K> taps = load_taps<T, K, VEC>(a, c0, n);
-  store4<T, VEC>((T *)a.y + r * a.y_stride + c0, n, conv_row<T, K>(a, taps, u));
+  F4 o[1] = {conv_row<T, K>(a, taps, u)};
+  if (NORM) norm_rows<T>(a, o);
+  store4<T, VEC>((T *)a.y + r * a.y_stride + c0, n, o[0]);
 #pragma unroll
   for (int i = 0; i < K - 1; ++i) store4<T, VEC>(entry + (int64_t)i * a.C, n, u[i + 1]);
 }
 
-// f(T, K, VEC) for the call's type, taps and alignment.
+// f(T, K, VEC, NORM) for the call's type, taps, alignment and norm.
 template <typename F>
 cudaError_t dispatch(const ConvArgs &a, F f) {
-#define KDA_CONV_CASE(TT, KK)                                   \
-  if (a.K == KK) return a.vec ? f.template run<TT, KK, true>() : f.template run<TT, KK, false>();
+#define KDA_CONV_CASE(TT, KK)                                                                            \
+  if (a.K == KK)                                                                                       \
+    return a.norm ? (a.vec ? f.template run<TT, KK, true, true>() : f.template run<TT, KK, false, true>()) \
+                  : (a.vec ? f.template run<TT, KK, true, false>() : f.template run<TT, KK, false, false>());
   if (a.bf16) {
     KDA_CONV_CASE(__nv_bfloat16, 2) KDA_CONV_CASE(__nv_bfloat16, 3) KDA_CONV_CASE(__nv_bfloat16, 4)
   } else {
@@ -365,12 +402,12 @@ cudaError_t dispatch(const ConvArgs &a, F f) {
   return cudaErrorInvalidValue;
 }
 
-// Rows of a tile: 64, or as few as let all tiles run at once (kBlocks an SM), but 8 at
+// Rows of a tile: 64, or as few as let all tiles run at once, but 8 at
 // least, as a tile costs about eight rows' instructions to begin.  4,096 x 2,048 with
 // norms: tiles of 16 rows (1,024 of them, a second wave of 136) took 18.3 us, of 20
 // 14 us.
 int conv_tile(const ConvArgs &a) {
-  const int64_t columns = (a.C + kThreads * V - 1) / (kThreads * V), at_once = kBlocks * 148;
+  const int64_t columns = (a.C + kThreads * V - 1) / (kThreads * V), at_once = blocks_of(a.norm) * 148;
   const int64_t tile = (columns * a.q.rows + at_once - 1) / at_once;
   return (int)(tile >= 64 ? 64 : tile <= 8 ? 8 : (tile + kGroup - 1) / kGroup * kGroup);
 }
@@ -378,11 +415,11 @@ int conv_tile(const ConvArgs &a) {
 struct RunConv {
   const ConvArgs &a;
   cudaStream_t st;
-  template <typename T, int K, bool VEC>
+  template <typename T, int K, bool VEC, bool NORM>
   cudaError_t run() const {
     const int tile = conv_tile(a);
     const dim3 grid((unsigned)(((int64_t)a.q.rows + tile - 1) / tile), (a.C + kThreads * V - 1) / (kThreads * V));
-    short_conv_kernel<T, K, VEC><<<grid, kThreads, 0, st>>>(a, tile);
+    short_conv_kernel<T, K, VEC, NORM><<<grid, kThreads, 0, st>>>(a, tile);
     return cudaGetLastError();
   }
 };
@@ -390,10 +427,10 @@ struct RunConv {
 struct RunStep {
   const ConvArgs &a;
   cudaStream_t st;
-  template <typename T, int K, bool VEC>
+  template <typename T, int K, bool VEC, bool NORM>
   cudaError_t run() const {
     const dim3 grid(a.q.R, (a.C + kThreads * V - 1) / (kThreads * V));
-    short_conv_step_kernel<T, K, VEC><<<grid, kThreads, 0, st>>>(a);
+    short_conv_step_kernel<T, K, VEC, NORM><<<grid, kThreads, 0, st>>>(a);
     return cudaGetLastError();
   }
 };

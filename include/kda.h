@@ -463,8 +463,10 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
  *   y   : [rows, H, P] dtype, y_stride
  *   H % G == 0;  N, P : each one of 16, 32, 64, 128
  * d_t A[h] <= 0 is relied on (d_t >= 0, which softplus gives).  State,
- * decays and sums are fp32; on the tensor-core path (bf16) products take bf16
- * operands as noted at the kernel.
+ * decays and sums are fp32; on the tensor-core path (bf16 with 16-byte aligned
+ * rows) the products take bf16 operands, as noted at the kernel, and an input
+ * that is not finite leaves its sequence's outputs undefined from up to 127
+ * tokens before it (from the last multiple of 128 of the position) on.
  *
  * State snapshots (section 5.4.1): with page_size > 0 (a multiple of 128) the
  * state after every position that is a multiple of page_size (counted with
