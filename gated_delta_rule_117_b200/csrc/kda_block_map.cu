@@ -19,7 +19,10 @@ constexpr int kThreads = 256;
 constexpr int kRowsPerBlock = 1024;
 constexpr int kMaxR = 16384;
 
-__device__ __forceinline__ int64_t blocks_of(int64_t tokens, int page) { return (tokens + page - 1) / page; }
+// Blocks of `tokens` tokens (a context and new tokens: below 2^32, so 32-bit divisions do).
+__device__ __forceinline__ uint32_t blocks_of(uint32_t tokens, uint32_t page) {
+  return tokens ? (tokens - 1) / page + 1 : 0;
+}
 
 __device__ __forceinline__ int saturate(int64_t v) { return v > INT32_MAX ? INT32_MAX : (int)v; }
 
@@ -35,9 +38,9 @@ __global__ void __launch_bounds__(kThreads) block_map_kernel(MapArgs a) {
     const int r = r0 + tid;
     int64_t n = 0, b = 0;
     if (r < a.R) {
-      n = max(a.len[r], 0);
-      const int64_t c = a.ctx ? max(a.ctx[r], 0) : 0;
-      b = blocks_of(c + n, a.page) - blocks_of(c, a.page);
+      const uint32_t len = max(a.len[r], 0), c = a.ctx ? max(a.ctx[r], 0) : 0;
+      n = len;
+      b = blocks_of(c + len, a.page) - blocks_of(c, a.page);
     }
     int64_t in = n, ib = b;
 #pragma unroll
@@ -90,19 +93,18 @@ __global__ void __launch_bounds__(kThreads) block_map_kernel(MapArgs a) {
         const int m = (lo + hi) >> 1;
         if (s_cu[m] <= row) lo = m; else hi = m;
       }
-      const int64_t c = a.ctx ? max(a.ctx[lo], 0) : 0;
-      const int64_t pos = c + row - s_cu[lo];
-      const int64_t j = pos / a.page;
-      const int64_t old = blocks_of(c, a.page);
-      if (j < a.table_stride) {
+      const uint32_t c = a.ctx ? max(a.ctx[lo], 0) : 0, page_size = a.page;
+      const uint32_t pos = c + (uint32_t)(row - s_cu[lo]);
+      const uint32_t j = pos / page_size, old = blocks_of(c, page_size);
+      if (j < (uint32_t)a.table_stride) {
         int64_t page = -1;
         if (j < old) {
           page = a.table[(int64_t)lo * a.table_stride + j];
         } else {
-          const int64_t f = s_new[lo] + (j - old);
+          const int64_t f = (int64_t)s_new[lo] + (j - old);
           if (f < a.n_free) page = a.free_pages[f];
         }
-        if (page >= 0) slot = page * a.page + pos % a.page;
+        if (page >= 0) slot = page * a.page + (pos - j * page_size);
       }
     }
     a.token_slots[row] = slot;

@@ -31,7 +31,7 @@
 //   warp 2       issues every MMA
 //   warps 4-11   scores: two threads own row t of G, half a block of columns each;
 //                they write W to TMEM
-//   warps 12-15  tokens: thread t writes row t of wx
+//   warps 12-15  tokens: thread t writes row t of wx (with warps 4-11, in a state pass)
 //   warps 16-23  state: two threads own row n of S, 32 columns (fp32 registers)
 //                each; they write the bf16 copy, the snapshots and the final state
 //   warps 24-31  outputs: two threads own row t of y, 32 columns each; a warp stores
@@ -249,10 +249,10 @@ __global__ void __launch_bounds__(NT, 1)
       uint32_t count = 1;  // TMA and MMA completions; the others count warps
       if (i == BX_FREE || i == BX_FREE + 1) count = kOut ? 9 : 1;  // the MMAs, and the output warps
       if (i >= DEC && i < DEC + 4) count = 2;
-      if (i >= DEC_FREE && i < DEC_FREE + 4) count = kOut ? 28 : 12;
+      if (i >= DEC_FREE && i < DEC_FREE + 4) count = kOut ? 28 : 20;
       if (i == TOTALS) count = 2;
       if (i == W_READY) count = 8;
-      if (i == WX_READY) count = 12;  // token and state warps
+      if (i == WX_READY) count = kOut ? 12 : 20;  // token and state warps
       if (i == YX_READY) count = 16;  // state and output warps
       mbar_init(&x.bar[i], count);
     }
@@ -514,8 +514,12 @@ __global__ void __launch_bounds__(NT, 1)
       x.arrive(DEC + (i & 3));
     }
     if (!kOut && b0 == 0 && lane == 0 && p0 == 0) p.decays[it.item * a.H + h] = ex2(total);
-  } else if (warp >= 12 && warp < 16) {
+  } else if ((warp >= 12 && warp < 16) || (!kOut && warp >= 4 && warp < 12)) {
     // ======================= tokens =======================
+    // 16-byte chunks of row t that this thread writes: all, or in a state pass, where the score
+    // warps have nothing else to do, a third or so (1.4 us a chunk with four warps alone)
+    const bool first = warp >= 12;
+    const int k0 = first ? 0 : 2 + 3 * ((warp - 4) >> 2), k1 = kOut ? 8 : first ? 2 : k0 + 3;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const bool live = t < ch.count(i);
@@ -528,8 +532,8 @@ __global__ void __launch_bounds__(NT, 1)
       auto load = [&](int k) {
         return live ? *reinterpret_cast<const uint4 *>(xt + sw128_chunk(t, k)) : make_uint4(0, 0, 0, 0);
       };
-      uint4 v = load(0);
-      if (!live) {  // rows behind the last token: x and B sum over tokens, so they must be zeros
+      uint4 v = load(k0);
+      if (first && !live) {  // rows behind the last token: x and B sum over tokens, so they must be zeros
         const uint4 z = make_uint4(0, 0, 0, 0);
         unsigned char *bt = sm + kB + (i & 1) * 32768;
 #pragma unroll 1
@@ -542,7 +546,7 @@ __global__ void __launch_bounds__(NT, 1)
       }
       if (i >= 1 && !x.wait(DS_DONE, i - 1)) break;  // wx is read
 #pragma unroll 2
-      for (int k = 0; k < 8; ++k) {
+      for (int k = k0; k < k1; ++k) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
         v = load((k + 1) & 7);
         uint32_t q0[4], q1[4], q2[4];
