@@ -16,13 +16,20 @@
 // row and a column part, so exponentials are taken for the diagonal blocks only.
 //
 // Rounding.  The state lives in fp32 registers; what is added to it is split into
-// three bf16 terms (24 bits), so the state keeps fp32 accuracy: one bf16 would put
-// 2^-9 of every update into it for good, and two leave 3e-6.  W and the copy of S
-// that outputs read are single bf16: each costs an output less than its own
-// rounding to bf16 does, and nothing carries on.
+// three bf16 terms (24 bits), so the state keeps fp32 accuracy: one bf16 would be off
+// by up to 2^-8 of every update for good, and two by 2^-16.  W and the copy of S that
+// outputs read are single bf16: what they cost an output (2.1e-3 of it in the mean
+// square, with its own rounding, against 1.7e-3 for that rounding alone) is not carried on.
 //
-// What bounds it: 1.8 K cycles of tensor-core work a chunk (0.95 us) against 32 KB
-// of x and y from HBM (0.74 us at the copy rate), and the handovers below.
+// What bounds it: shared memory.  A chunk's products read 208 KB of it (with N = 64
+// columns an operand pair feeds the tensor core at 48 cycles a step for its 32), loads
+// and stores by TMA move 96 KB and the roles 128 KB: 3,400 cycles at 128 bytes a cycle.
+// Measured, 148 CTAs, N = 128: 4,100 to 4,300 cycles, 2.3 us a chunk (against 0.74 us
+// for its 32 KB of x and y at the copy rate), tensor pipe 47 % and issue slots 56 %
+// busy.  What was tried and lost: rows of y stored from registers instead of a staged
+// tile (2.99 us), the scores' diagonal factors before G or the outputs' tensor memory
+// read at once (2.35 and 2.42 against 2.33), the score warps sharing wx in output runs
+// (3.03).  Two terms instead of three are 7 % faster and lose the state's last 8 bits.
 //
 // Work split: one CTA a (segment, head, 64 columns of P), 32 warps of 64 registers:
 //   warp 0       producer: TMA loads of B, x (two stages) and C
@@ -36,10 +43,10 @@
 //                each; they write the bf16 copy, the snapshots and the final state
 //   warps 24-31  outputs: two threads own row t of y, 32 columns each; a warp stores
 //                its tile by TMA
-// The order of a chunk's products lets each role work under the others' tensor
-// time: scores under Yx and dS, the state update under Yi and the next G.  C is
-// single-buffered (its last reader, Yx, comes early), which makes room for wx's
-// third term; B and x have two stages.
+// The order of a chunk's products, Yx, G, dS, Yi, lets the roles work under the tensor
+// time of others: scores under dS, the state update under Yi.  C is single-buffered
+// (its readers come first), which makes room for wx's third term; B and x have two
+// stages.
 // Columns of S are independent, so P = 128 is two CTAs (which form G twice: it
 // is a third of the tensor work and saves any exchange).  Rows behind a chunk's
 // last token are zeroed in the operands that sum over tokens, and not stored;
@@ -517,7 +524,7 @@ __global__ void __launch_bounds__(NT, 1)
   } else if ((warp >= 12 && warp < 16) || (!kOut && warp >= 4 && warp < 12)) {
     // ======================= tokens =======================
     // 16-byte chunks of row t that this thread writes: all, or in a state pass, where the score
-    // warps have nothing else to do, a third or so (1.4 us a chunk with four warps alone)
+    // warps have nothing else to do, two or three of the eight
     const bool first = warp >= 12;
     const int k0 = first ? 0 : 2 + 3 * ((warp - 4) >> 2), k1 = kOut ? 8 : first ? 2 : k0 + 3;
 #pragma unroll 1

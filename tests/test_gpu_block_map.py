@@ -55,6 +55,23 @@ def test_too_few_blocks_or_columns():
     _check(lens, c, free[:0], table, 8, int(lens.sum()))
 
 
+def test_more_requests_than_a_block_has_threads_many_times():
+    lens, c, free, table = _case(16384, 3, 2, 11)
+    _check(lens, c, free, table, 2, int(lens.sum()))
+
+
+def test_lengths_that_do_not_add_up_to_32_bits():
+    # sums saturate, and nothing is written outside
+    R = 4
+    lens = np.array([5, 2**31 - 1, 2**31 - 1, 7], np.int32)
+    d = lambda v: torch.tensor(v, dtype=torch.int32, device="cuda")
+    table = torch.full((R, 3), -9, dtype=torch.int32, device="cuda")
+    cu, slots, used = kda.block_map(d(lens.tolist()), None, d(list(range(50))), table, 1, 40)
+    assert cu.tolist() == [0, 5, 2**31 - 1, 2**31 - 1, 2**31 - 1] and int(used) == 2**31 - 1
+    assert table.tolist() == [[0, 1, 2], [5, 6, 7], [-1] * 3, [-1] * 3]
+    assert slots.tolist() == [0, 1, 2, -1, -1, 5, 6, 7] + [-1] * 32
+
+
 def test_negative_lengths_count_as_none():
     lens, c, free, table = _case(9, 30, 8, 9)
     lens[3] = -5
