@@ -104,7 +104,7 @@ template <typename F>
 __device__ __forceinline__ int block_count_le(int n, F key, int v) {
   int lo = 0, hi = n;  // the count lies in [lo, hi]
   while (lo < hi) {
-    const int step = (hi - lo + blockDim.x - 1) / blockDim.x;
+    const int step = (hi - lo - 1) / (int)blockDim.x + 1;
     const int64_t i = lo + (int64_t)threadIdx.x * step;
     const int c = __syncthreads_count(i < hi && key((int)i) <= v);
     if (c == 0) return lo;

@@ -11,6 +11,7 @@ namespace {
 using namespace kda::check;
 
 constexpr int kMaxMapRequests = 16384;
+constexpr int kMaxRows = INT32_MAX - 4096;      // rows and what is added to them stay 32-bit
 constexpr int kMaxChannels = 1 << 24;  // a block for each 512 of them in a grid's second dimension
 
 size_t elem(kda_dtype_t t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
@@ -18,6 +19,11 @@ size_t elem(kda_dtype_t t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
 // Bytes between the first and the last element of a token-major array.
 size_t extent(int64_t rows, int64_t stride, int64_t width, size_t e) {
   return rows > 0 ? (size_t)((rows - 1) * stride + width) * e : 0;
+}
+
+// Whether a row stride holds `width` elements and the array's extent an int64.
+bool stride_fits(int64_t rows, int64_t stride, int64_t width) {
+  return stride >= width && stride <= (int64_t(1) << 48) / (rows > 0 ? rows : 1);
 }
 
 // Whether any of `outs` overlaps another of them or one of `ins`.
@@ -38,14 +44,14 @@ bool aligned4(const void *p) { return aligned_to(p, 4); }
 kda_status_t check_requests(int R, int rows, const int *cu, const int *ctx, const int *slots, const void *state,
                             int n_slots) {
   if (R < 0 || rows < 0 || n_slots < 0) return KDA_ERR_INVALID_ARG;
-  if (!cu && R > 0 && rows % R != 0) return KDA_ERR_SHAPE;
+  if (rows > kMaxRows || (!cu && R > 0 && rows % R != 0)) return KDA_ERR_SHAPE;
   if ((state != nullptr) != (n_slots > 0)) return KDA_ERR_INVALID_ARG;
   if (state && !slots && n_slots < R) return KDA_ERR_SHAPE;
   if (!aligned4(cu) || !aligned4(ctx) || !aligned4(slots)) return KDA_ERR_ALIGNMENT;
   return KDA_OK;
 }
 
-kda_status_t check_conv(const void *x, int64_t x_stride, const void *w, const void *bias, const void *state, void *y,
+kda_status_t check_conv(int rows, const void *x, int64_t x_stride, const void *w, const void *bias, const void *state, void *y,
                         int64_t y_stride, int C, int K, int head_dim, kda_dtype_t dtype, int flags, float eps) {
   if (C < 0) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_DTYPE;
@@ -54,7 +60,8 @@ kda_status_t check_conv(const void *x, int64_t x_stride, const void *w, const vo
   const bool heads = (flags & (KDA_CONV_L2NORM | KDA_CONV_HEAD_MAJOR)) != 0;
   if (heads && (!supported_d(head_dim) || C % head_dim != 0)) return KDA_ERR_SHAPE;
   if ((flags & KDA_CONV_L2NORM) && (!(eps >= 0.f) || !isfinite(eps))) return KDA_ERR_INVALID_ARG;
-  if (x_stride < C || (!(flags & KDA_CONV_HEAD_MAJOR) && y_stride < C)) return KDA_ERR_SHAPE;
+  if (!stride_fits(rows, x_stride, C) || (!(flags & KDA_CONV_HEAD_MAJOR) && !stride_fits(rows, y_stride, C)))
+    return KDA_ERR_SHAPE;
   const size_t e = elem(dtype);
   const void *ptrs[] = {x, w, bias, state, y};
   for (const void *p : ptrs)
@@ -86,7 +93,7 @@ kda_status_t kda_block_map(const int *len, const int *ctx, const int *free_pages
                            int table_stride, int page_size, int *cu, int64_t *token_slots, int *pages_used, int R,
                            int rows, kda_stream_t stream) {
   if (R < 0 || rows < 0 || n_free < 0 || table_stride < 0 || page_size < 1) return KDA_ERR_INVALID_ARG;
-  if (R > kMaxMapRequests) return KDA_ERR_SHAPE;
+  if (R > kMaxMapRequests || rows > kMaxRows) return KDA_ERR_SHAPE;
   if (!cu || !pages_used || (R > 0 && !len) || (n_free > 0 && !free_pages) ||
       (R > 0 && table_stride > 0 && !block_table) || (rows > 0 && !token_slots))
     return KDA_ERR_INVALID_ARG;
@@ -114,7 +121,7 @@ kda_status_t kda_short_conv(const void *x, int64_t x_stride, const void *w, cons
                             int C, int K, int head_dim, kda_dtype_t dtype, int flags, float eps, kda_stream_t stream) {
   kda_status_t st = check_requests(R, rows, cu, ctx, slots, state, n_slots);
   if (st != KDA_OK) return st;
-  st = check_conv(x, x_stride, w, bias, state, y, y_stride, C, K, head_dim, dtype, flags, eps);
+  st = check_conv(rows, x, x_stride, w, bias, state, y, y_stride, C, K, head_dim, dtype, flags, eps);
   if (st != KDA_OK) return st;
   const bool head_major = (flags & KDA_CONV_HEAD_MAJOR) != 0;
   if (head_major && cu) return KDA_ERR_INVALID_ARG;
@@ -149,9 +156,9 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
                                  int head_dim, kda_dtype_t dtype, int flags, float eps, kda_stream_t stream) {
   kda_status_t st = check_requests(R, R, nullptr, nullptr, slots, state, n_slots);
   if (st != KDA_OK) return st;
-  st = check_conv(x, x_stride, w, bias, state, y, y_stride, C, K, head_dim, dtype, flags, eps);
+  st = check_conv(R, x, x_stride, w, bias, state, y, y_stride, C, K, head_dim, dtype, flags, eps);
   if (st != KDA_OK) return st;
-  if (y_stride < C) return KDA_ERR_SHAPE;
+  if (!stride_fits(R, y_stride, C)) return KDA_ERR_SHAPE;
   if (R == 0 || C == 0) return KDA_OK;
   if (!x || !w || !y || !state) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dtype);
@@ -191,7 +198,8 @@ kda_status_t check_ssm_sizes(int H, int G, int N, int P, kda_dtype_t dtype) {
 // The arguments that the scan and the step share.  `rows`: of the token-major arrays.
 kda_status_t check_ssm(const kda::SsmArgs &a, int rows, size_t workspace, kda_dtype_t dtype) {
   const int64_t HP = (int64_t)a.H * a.P, GN = (int64_t)a.G * a.N;
-  if (a.x_stride < HP || a.y_stride < HP || a.dt_stride < a.H || a.b_stride < GN || a.c_stride < GN)
+  if (!stride_fits(rows, a.x_stride, HP) || !stride_fits(rows, a.y_stride, HP) || !stride_fits(rows, a.dt_stride, a.H) ||
+      !stride_fits(rows, a.b_stride, GN) || !stride_fits(rows, a.c_stride, GN))
     return KDA_ERR_SHAPE;
   if (!a.x || !a.dt || !a.A || !a.B || !a.C || !a.y) return KDA_ERR_INVALID_ARG;
   const size_t e = elem(dtype);

@@ -360,6 +360,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(NORM)) short_conv_kernel(C
     }
     ++r;
   }
+  if (VEC) asm volatile("cp.async.wait_all;" ::: "memory");  // nothing in flight at the block's end
 }
 
 template <typename T, int K, bool VEC, bool NORM>

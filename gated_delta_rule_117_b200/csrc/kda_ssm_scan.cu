@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
 
   // blocks of TB tokens that end at multiples of TB of the position, so snapshots fall on their ends
   for (int t0 = it.begin, nt; t0 < it.end; t0 += nt) {
-    nt = min(TB - (it.s.ctx + t0) % TB, it.end - t0);
+    nt = min(TB - (int)(((uint32_t)it.s.ctx + (uint32_t)t0) % TB), it.end - t0);
     const int64_t row0 = (int64_t)it.s.start + t0;
     __syncthreads();
     for (int e = tid; e < nt * N; e += NT) {

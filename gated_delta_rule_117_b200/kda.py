@@ -511,7 +511,7 @@ def _at(t):
 def _rows(name, t, lead):
     """Row stride of token-major `t`: `lead` leading dimensions of rows over dense rows of elements."""
     if lead == 1 and t.is_contiguous():
-        return t.stride(0) if t.size(0) > 1 else t.numel()
+        return t.numel() if t.size(0) == 1 else t.stride(0)
     shape, stride = t.shape, t.stride()
     want = 1
     for i in range(len(shape) - 1, lead - 1, -1):
@@ -607,11 +607,11 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
         raise ValueError("lens and ctx must be [R], free_pages [n], block_table [R, blocks]")
     given = cu is not None or token_slots is not None or pages_used is not None
     if cu is None:
-        cu = lens.new_empty(R + 1)
+        cu = _fresh(stream, lens.new_empty, R + 1)
     if token_slots is None:
-        token_slots = lens.new_empty(rows, dtype=torch.int64)
+        token_slots = _fresh(stream, lens.new_empty, rows, dtype=torch.int64)
     if pages_used is None:
-        pages_used = lens.new_empty(1)
+        pages_used = _fresh(stream, lens.new_empty, 1)
     if given:
         _shaped("cu", cu, (R + 1,))
         _shaped("token_slots", token_slots, (rows,))
@@ -626,10 +626,23 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
     return cu, token_slots, pages_used
 
 
-def _output(x, y, lead, width):
+def _on_stream(stream):
+    """A context whose allocations belong to the stream that will use them (`stream`: a torch stream or a handle)."""
+    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(stream))
+
+
+def _fresh(stream, make, *args, **kw):
+    """make(*args, **kw): a tensor that belongs to the call's stream (None: the current one)."""
+    if stream is None:
+        return make(*args, **kw)
+    with _on_stream(stream):
+        return make(*args, **kw)
+
+
+def _output(x, y, lead, width, stream):
     """(y, its row stride) for a token-major output like x."""
     if y is None:
-        return _torch.empty_like(x, memory_format=_torch.contiguous_format), width
+        return _fresh(stream, _torch.empty_like, x, memory_format=_torch.contiguous_format), width
     _typed(x.dtype, "y", y)
     _shaped("y", y, x.shape)
     _on(x, y)
@@ -667,13 +680,13 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
     K = _conv_weights(x, w, bias, state, C, d)
     R, rows = _requests(x, lead, slots, ctx, cu, d)
     if not head_major:
-        y, ys = _output(x, y, lead, C)
+        y, ys = _output(x, y, lead, C, stream)
     else:
         if head_dim <= 0 or C % head_dim:
             raise ValueError("head_major needs a head_dim that divides C")
         shape, ys = (R, C // head_dim, rows // max(R, 1), head_dim), C
         if y is None:
-            y = torch.empty(shape, dtype=x.dtype, device=x.device)
+            y = _fresh(stream, torch.empty, shape, dtype=x.dtype, device=x.device)
         else:
             _typed(x.dtype, "y", y)
             _shaped("y", y, shape)
@@ -699,7 +712,7 @@ def short_conv_step(x, w, state, bias=None, *, slots=None, silu=True, head_dim=0
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
-    y, ys = _output(x, y, 1, C)
+    y, ys = _output(x, y, 1, C, stream)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0)
     _launch(load_library().kda_short_conv_step, "kda_short_conv_step", d, stream,
             (x.data_ptr(), _rows("x", x, 1), w.data_ptr(), _at(bias), state.data_ptr(), state.size(0), _at(slots),
@@ -760,14 +773,15 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
         _shaped("pages", pages, (n_pages, H, N, P))
     else:
         block_table = pages = None
-    y, ys = _output(x, y, lead, H * P)
+    y, ys = _output(x, y, lead, H * P, stream)
     lib = load_library()
     ws = lib.kda_ssm_scan_workspace_size(R, rows, H, G, N, P, code)
     if ws == (1 << 64) - 1:
         raise KdaError(2, "kda_ssm_scan_workspace_size")
     wbytes = 0
     if ws > 0 and workspace is None:
-        workspace = torch.empty(ws, dtype=torch.uint8, device=x.device)
+        # (it is given back when this returns, maybe before the stream is done with it)
+        workspace = _fresh(stream, torch.empty, ws, dtype=torch.uint8, device=x.device)
     if workspace is not None:
         _dense("workspace", workspace)
         _on(x, workspace)
@@ -792,7 +806,7 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, softplus=True, slot
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
-    y, ys = _output(x, y, 1, H * P)
+    y, ys = _output(x, y, 1, H * P, stream)
     _launch(load_library().kda_ssm_step, "kda_ssm_step", d, stream,
             (x.data_ptr(), xs, dt.data_ptr(), ds, A.data_ptr(), B.data_ptr(), bs, C.data_ptr(), cs, _at(D), _at(dt_bias),
              1 if softplus else 0, state.data_ptr(), state.size(0), _at(slots), y.data_ptr(), ys, R, H, G, N, P, code))

@@ -349,7 +349,7 @@ size_t kda_noalloc_scratch_bytes(void);
  * The calls below work on R sequences ("requests") whose tokens lie one after
  * another in the rows of token-major arrays, and whose states lie in a pool.
  * They share these arguments:
- *   R, rows  : sequences, and rows of the token-major arrays
+ *   R, rows  : sequences, and rows of the token-major arrays (at most 2^31 - 4097)
  *   cu       : [R + 1] int32, non-decreasing; sequence r owns rows cu[r] ..
  *              cu[r + 1] - 1 (none is allowed), and cu[R] <= rows.  Rows before
  *              cu[0] and from cu[R] on belong to no sequence: what they hold

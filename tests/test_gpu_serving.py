@@ -276,6 +276,60 @@ def test_offsets_beyond_32_bits():
     assert torch.equal(pool[4299], small[0]) and torch.equal(pool[4290], small[1]) and pool[0].abs().sum() == 0
 
 
+def test_workspace_of_a_named_stream():
+    # the helper's own workspace is freed when it returns: what the current stream allocates then must not
+    # share it with the call that still runs on the other stream
+    ins = _scan_inputs(20000, 2, 128, 128, BF, 5)
+    assert kda.kda_ssm_scan_workspace_size(1, 20000, 2, 1, 128, 128, kda.KDA_DTYPE_BF16) > 0
+    ref = kda.ssm_scan(*ins)
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    ys = []
+    for handle in (other, other.cuda_stream) * 4:
+        ys.append(kda.ssm_scan(*ins, stream=handle))
+        junk = [torch.full((n,), float("nan"), device="cuda") for n in (1 << 18, 1 << 20, 1 << 22)]
+        del junk
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, ref) for y in ys)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_contexts_up_to_the_largest(dtype):
+    # positions near 2^31 and beyond it: the same states and outputs, and the snapshots at multiples of page
+    H, N, P, T = 2, 64, 64, 300
+    x, dt, A, B, C, D, bias = _scan_inputs(T, H, N, P, dtype, 4)
+    pool = torch.randn(1, H, N, P, device="cuda")
+    want = pool.clone()
+    ref = kda.ssm_scan(x, dt, A, B, C, D, bias, state=want, ctx=_i32([123]))  # 123 = (2^31 - 5) % 128
+    ctx = 2**31 - 5
+    pages, table = torch.zeros(2, H, N, P, device="cuda"), _i32([[0, 1]])
+    y = kda.ssm_scan(x, dt, A, B, C, D, bias, state=pool, ctx=_i32([ctx]), block_table=table, pages=pages, page_size=1 << 30)
+    torch.cuda.synchronize()
+    assert rel_l2(y, _n(ref)) <= TOL[dtype] and rel_l2(pool, _n(want)) <= TOL[F32]
+    assert pages[0].abs().sum() == 0 and pages[1].abs().sum() > 0  # 2^31 is the end of block 1
+    w = torch.randn(H * P, 4, device="cuda").to(dtype)
+    a, b = torch.ones(1, 3, H * P, dtype=dtype, device="cuda"), torch.ones(1, 3, H * P, dtype=dtype, device="cuda")
+    ya = kda.short_conv(x.flatten(1), w, state=a, ctx=_i32([2**31 - 1]))
+    yb = kda.short_conv(x.flatten(1), w, state=b, ctx=_i32([1]))
+    assert torch.equal(ya, yb) and torch.equal(a, b) and kda.kda_get_device_status() == 0
+
+
+def test_empty_calls():
+    z = lambda *s, dtype=BF: torch.zeros(*s, dtype=dtype, device="cuda")
+    none = _i32([])
+    assert kda.short_conv(z(0, 64), z(64, 4), cu=_i32([0, 0, 0])).shape == (0, 64)
+    assert kda.short_conv(z(2, 0, 64), z(64, 4), head_dim=32, head_major=True).shape == (2, 2, 0, 32)
+    assert kda.short_conv_step(z(0, 64), z(64, 4), z(3, 3, 64), slots=none).shape == (0, 64)
+    a = torch.ones(2, device="cuda")
+    assert kda.ssm_scan(z(0, 2, 16), z(0, 2), a, z(0, 1, 16), z(0, 1, 16)).shape == (0, 2, 16)
+    assert kda.ssm_scan(z(3, 0, 2, 16), z(3, 0, 2), a, z(3, 0, 1, 16), z(3, 0, 1, 16)).shape == (3, 0, 2, 16)
+    pool = z(1, 2, 16, 16, dtype=F32)
+    assert kda.ssm_step(z(0, 2, 16), z(0, 2), a, z(0, 1, 16), z(0, 1, 16), pool, slots=none).shape == (0, 2, 16)
+    cu, slots, used = kda.block_map(none, None, none, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), 16, 0)
+    torch.cuda.synchronize()
+    assert cu.tolist() == [0] and slots.numel() == 0 and used.tolist() == [0] and kda.kda_get_device_status() == 0
+
+
 def test_short_wait_limit_leaves_results_alone():
     # the scan's waits are bounded by the library's limit; an ordinary call never comes near it
     ins = _scan_inputs(2000, 8, 128, 64, BF, 2)

@@ -166,6 +166,13 @@ def test_ssm_step_rejects(over, code):
     assert _step(**over) == code
 
 
+def test_sizes_that_would_not_fit_their_arithmetic():
+    most = (1 << 31) - 4097
+    assert _conv(rows=most + 1) == SHAPE and _map(rows=most + 1) == SHAPE and _scan(rows=most + 1) == SHAPE
+    assert _conv(x_stride=1 << 48) == SHAPE and _scan(x_stride=1 << 48) == SHAPE and _scan(dt_stride=1 << 48) == SHAPE
+    assert _conv_step(y_stride=1 << 48) == SHAPE and _step(c_stride=1 << 48) == SHAPE
+
+
 def test_nothing_to_do():
     assert _conv(R=0, rows=0, x=None) == 0 and _conv(rows=0, y=None) == 0 and _conv_step(R=0) == 0
     assert _scan(R=0, rows=0, x=None) == 0 and _scan(H=0, y=None) == 0 and _step(R=0) == 0
