@@ -98,27 +98,48 @@ struct Decays {
 static_assert(kDec + 4 * sizeof(Decays) <= kBarOff && kSmemBytes <= 232448, "shared memory layout");
 
 enum {
-  F_BX = 0,   // [2] B and x landed
-  BX_FREE = 2,   // [2] every reader of B and x is done
+  F_BX = 0,   // [2] x landed, and B in an output run
+  BX_FREE = 2,   // [2] every reader of those is done
   DEC = 4,       // [4] decays written
   DEC_FREE = 8,  // [4] decays read by the other roles
   F_C = 12,   // C landed
   C_FREE,     // C read (Yx done)
   G_DONE,     // G in TMEM
   W_READY,    // W in TMEM (and G read)
-  WX_READY,   // wx written, tail rows zeroed; the dS before is read
-  DS_DONE,    // dS in TMEM (and wx and S read)
-  YX_READY,   // bf16 S of the chunk written; the Yi and Yx before are read
+  WX_READY,   // [2] wx written, tail rows zeroed; the dS that was in its place is read
+  DS_DONE = WX_READY + 2,  // [2] dS in TMEM (and wx and S read)
+  YX_READY = DS_DONE + 2,  // bf16 S of the chunk written; the Yi and Yx before are read
   Y_DONE,     // [2] Yi and Yx in TMEM (and W read)
   TOTALS = Y_DONE + 2,  // the blocks' totals are written
-  DRAIN,      // every MMA issued is done
+  F_B,        // [2] state pass: B landed
+  B_FREE = F_B + 2,  // [2] state pass: B read
+  DRAIN = B_FREE + 2,  // every MMA issued is done
   BARS
 };
 static_assert(kBarOff + 8 * BARS <= kMisc, "barriers");
 
 // TMEM columns
 constexpr uint32_t kCols = 512;
+// (state pass: dS twice, at 0 and 192)
 constexpr uint32_t tG = 0, tW = 128, tDS = 192, tYi = 384, tYx = 448;  // dS: one block of 64 for each term of wx
+
+// A state pass has no C, S or y, so it has room for two wx and two dS: wx of a chunk is
+// written while the products of the one before run.  And as its chunks are short against
+// the latency of their loads (2,300 cycles from a stage's release to its next tiles), x is
+// released when wx is written and B, which only the products read, on its own.  131,072
+// tokens, 16 heads of 128, 9 segments: 313 us with x and B released together and one wx.
+// Places and depth of each run:
+template <bool kOut>
+struct Layout {
+  static constexpr int B = kOut ? kB : 0, X = kOut ? kX : 65536, W = kOut ? kW : 98304;
+  static constexpr int kDeep = kOut ? 1 : 2;
+  static __device__ __forceinline__ int w(int i) { return W + (kOut ? 0 : (i & 1) * 49152); }
+  static __device__ __forceinline__ uint32_t ds(int i) { return kOut ? tDS : 192u * (i & 1); }
+  // entry of a ring of kDeep barriers, and its phase, for chunk i
+  static __device__ __forceinline__ int at(int i) { return kOut ? 0 : i & 1; }
+  static __device__ __forceinline__ int phase(int i) { return kOut ? i : i >> 1; }
+};
+static_assert(Layout<false>::W + 2 * 49152 <= kDec, "two wx in a state pass");
 
 struct TcArgs {
   SsmArgs a;
@@ -233,6 +254,7 @@ template <bool kOut, int NK>
 __global__ void __launch_bounds__(NT, 1)
     ssm_tc_kernel(const __grid_constant__ CUtensorMap mx, const __grid_constant__ CUtensorMap mb,
                   const __grid_constant__ CUtensorMap mc, const __grid_constant__ CUtensorMap my, const TcArgs p) {
+  using L = Layout<kOut>;
   extern __shared__ __align__(1024) unsigned char smraw[];
   const SsmArgs &a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -241,7 +263,7 @@ __global__ void __launch_bounds__(NT, 1)
   const bool tell = kOut && p0 == 0 && h == 0 && tid == 0;
   unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   Item it;
-  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, reinterpret_cast<int *>(sm + kW), it)) return;
+  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, reinterpret_cast<int *>(sm + L::W), it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const Chunks ch(it);
   const int n = ch.n, g = h / (a.H / a.G);
@@ -254,12 +276,12 @@ __global__ void __launch_bounds__(NT, 1)
   if (tid == 0) {
     for (int i = 0; i < BARS; ++i) {
       uint32_t count = 1;  // TMA and MMA completions; the others count warps
-      if (i == BX_FREE || i == BX_FREE + 1) count = kOut ? 9 : 1;  // the MMAs, and the output warps
-      if (i >= DEC && i < DEC + 4) count = 2;
+      if (i == BX_FREE || i == BX_FREE + 1) count = kOut ? 9 : 12;  // the MMAs and the output warps; the token warps
+      if (i >= DEC && i < DEC + 4) count = kOut ? 2 : 4;
       if (i >= DEC_FREE && i < DEC_FREE + 4) count = kOut ? 28 : 20;
-      if (i == TOTALS) count = 2;
+      if (i == TOTALS) count = kOut ? 2 : 4;
       if (i == W_READY) count = 8;
-      if (i == WX_READY) count = kOut ? 12 : 20;  // token and state warps
+      if (i == WX_READY || i == WX_READY + 1) count = kOut ? 12 : 20;  // token and state warps
       if (i == YX_READY) count = 16;  // state and output warps
       mbar_init(&x.bar[i], count);
     }
@@ -283,21 +305,28 @@ __global__ void __launch_bounds__(NT, 1)
   if (warp == 0) {
     // ======================= producer =======================
     const uint32_t half = NK > 4 ? 32768u : 16384u;  // bytes of a B or C tile that are loaded
-    int loads = 0, cloads = 0;
+    int loads = 0, bloads = 0, cloads = 0;
     bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1, row = row_of_seq + ch.first(i);
       if (i >= 2 && !(ok = x.wait2(BX_FREE, i - 2))) break;
+      const int f_b = kOut ? F_BX : F_B;
       if (elect_one()) {
-        mbar_arrive_expect_tx(&x.bar[F_BX + st], half + 16384u);
-        tma_load_3d(sm + kX + st * 16384, &mx, &x.bar[F_BX + st], p0, h, row);
-#pragma unroll
-        for (int c = 0; c < 16 * NK; c += 64)
-          tma_load_3d(sm + kB + st * 32768 + c * 256, &mb, &x.bar[F_BX + st], c, g, row);
+        mbar_arrive_expect_tx(&x.bar[F_BX + st], 16384u + (kOut ? half : 0u));
+        tma_load_3d(sm + L::X + st * 16384, &mx, &x.bar[F_BX + st], p0, h, row);
       }
       __syncwarp();
       loads = i + 1;
+      if (!kOut && i >= 2 && !(ok = x.wait2(B_FREE, i - 2))) break;
+      if (elect_one()) {
+        if (!kOut) mbar_arrive_expect_tx(&x.bar[f_b + st], half);
+#pragma unroll
+        for (int c = 0; c < 16 * NK; c += 64)
+          tma_load_3d(sm + L::B + st * 32768 + c * 256, &mb, &x.bar[f_b + st], c, g, row);
+      }
+      __syncwarp();
+      bloads = i + 1;
       if (kOut) {
         if (i >= 1 && !(ok = x.wait(C_FREE, i - 1))) break;
         if (elect_one()) {
@@ -323,10 +352,14 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if (!ok) {  // loads in flight must land before shared memory is given up
       const uint64_t t0 = global_ns();
+      auto landed = [&](int b, int n) {  // the last two of n loads
 #pragma unroll 1
-      for (int k = max(0, loads - 2); k < loads; ++k)
-        while (!mbar_try_wait_sleep(&x.bar[F_BX + (k & 1)], (k >> 1) & 1, 1000000u))
-          if (global_ns() - t0 > p.wait_ns) break;
+        for (int k = max(0, n - 2); k < n; ++k)
+          while (!mbar_try_wait_sleep(&x.bar[b + (k & 1)], (k >> 1) & 1, 1000000u))
+            if (global_ns() - t0 > p.wait_ns) break;
+      };
+      landed(F_BX, loads);
+      if (!kOut) landed(F_B, bloads);
       if (cloads > 0)
         while (!mbar_try_wait_sleep(&x.bar[F_C], (cloads - 1) & 1, 1000000u))
           if (global_ns() - t0 > p.wait_ns) break;
@@ -337,17 +370,16 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t idYx = idesc_bf16(128, 64, false, true, false);
     const uint32_t idDS = idesc_bf16(128, 192, true, true, false);  // the terms of wx side by side
     const uint64_t dS = sdesc_sw128(sbase + kS, 16, 1024);
-    const uint64_t dW = sdesc_sw128(sbase + kW, 16384, 1024);
     const uint64_t dC = sdesc_sw128(sbase + kC, 16, 1024);
     // byte offset of K step k in a [128 x 128] tile, K along its rows
     auto koff = [](int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32); };
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
-      const uint64_t dB = sdesc_sw128(sbase + kB + st * 32768, 16, 1024);
-      const uint64_t dBt = sdesc_sw128(sbase + kB + st * 32768, 16384, 1024);
-      const uint64_t dX = sdesc_sw128(sbase + kX + st * 16384, 16, 1024);
-      if (!x.wait2(F_BX, i)) break;
+      const uint64_t dB = sdesc_sw128(sbase + L::B + st * 32768, 16, 1024);
+      const uint64_t dBt = sdesc_sw128(sbase + L::B + st * 32768, 16384, 1024);
+      const uint64_t dX = sdesc_sw128(sbase + L::X + st * 16384, 16, 1024);
+      if (!x.wait2(kOut ? F_BX : F_B, i)) break;
       if (kOut) {
         // (the G before was read before its W was ready)
         // Yx first: it waits longest for what it reads, and C is free for the next chunk once both
@@ -364,13 +396,15 @@ __global__ void __launch_bounds__(NT, 1)
         }
         __syncwarp();
       }
-      if (!x.wait(WX_READY, i)) break;
+      if (!x.wait(WX_READY + L::at(i), L::phase(i))) break;
       tc_fence_after();
+      const uint64_t dW = sdesc_sw128(sbase + L::w(i), 16384, 1024);
       if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) mma_bf16(tb + tDS, sdesc_add(dBt, k * 2048), sdesc_add(dW, k * 2048), idDS, k > 0);
-        mma_commit(&x.bar[DS_DONE]);
-        if (!kOut) mma_commit(&x.bar[BX_FREE + st]);
+        for (int k = 0; k < 8; ++k)
+          mma_bf16(tb + L::ds(i), sdesc_add(dBt, k * 2048), sdesc_add(dW, k * 2048), idDS, k > 0);
+        mma_commit(&x.bar[DS_DONE + L::at(i)]);
+        if (!kOut) mma_commit(&x.bar[B_FREE + st]);
       }
       __syncwarp();
       if (kOut) {
@@ -448,36 +482,46 @@ __global__ void __launch_bounds__(NT, 1)
       x.arrive(W_READY);
       x.arrive(DEC_FREE + (i & 3));
     }
-  } else if (warp < 4) {
-    // ======================= decays (warps 1 and 3) =======================
-    const int b0 = warp & 2;  // this warp's blocks: b0, b0 + 1
+  } else if (kOut ? warp < 4 : warp >= 24 && warp < 28) {
+    // ======================= decays =======================
+    // two blocks of 32 tokens for each of warps 1 and 3; in a state pass, whose chunks are shorter,
+    // one for each of warps 24-27
+    constexpr int NB = kOut ? 2 : 1, kAhead = 3;
+    const int b0 = kOut ? warp & 2 : warp & 3;  // this warp's blocks: b0 ..
     const float A2 = a.A[h] * 1.4426950408889634f;
     const __nv_bfloat16 *dt = (const __nv_bfloat16 *)a.dt + h;
     const float bias = a.dt_bias ? a.dt_bias[h] : 0.f;
-    float raw[2], total = 0.f;
-    auto fetch = [&](int i) {
+    // dt of the next chunks, as loaded (a conversion here would wait for the load, which takes about
+    // as long as a chunk)
+    __nv_bfloat16 raw[NB][kAhead];
+    float total = 0.f;
+    auto fetch = [&](int i, int to) {
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NB; ++k) {
         const int tk = 32 * (b0 + k) + lane;
-        raw[k] = i < n && tk < ch.count(i) ? __bfloat162float(dt[(int64_t)(row_of_seq + ch.first(i) + tk) * a.dt_stride]) : 0.f;
+        raw[k][to] = __ushort_as_bfloat16(0);
+        if (i < n && tk < ch.count(i)) raw[k][to] = dt[(int64_t)(row_of_seq + ch.first(i) + tk) * a.dt_stride];
       }
     };
-    fetch(0);
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) fetch(j, j);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      float d[2], up[2], s[2];
+      float d[NB], up[NB], s[NB];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        d[k] = raw[k] + bias;
+      for (int k = 0; k < NB; ++k) {
+        d[k] = __bfloat162float(raw[k][0]) + bias;
+#pragma unroll
+        for (int j = 0; j + 1 < kAhead; ++j) raw[k][j] = raw[k][j + 1];
         if (a.softplus) d[k] = softplus_fast(d[k]);
         if (32 * (b0 + k) + lane >= ch.count(i)) d[k] = 0.f;
         up[k] = s[k] = d[k] * A2;
       }
-      fetch(i + 1);
+      fetch(i + kAhead, kAhead - 1);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
+        for (int k = 0; k < NB; ++k) {
           const float u = __shfl_up_sync(~0u, up[k], o), v = __shfl_down_sync(~0u, s[k], o);
           if (lane >= o) up[k] += u;
           if (lane + o < 32) s[k] += v;
@@ -486,7 +530,7 @@ __global__ void __launch_bounds__(NT, 1)
       if (i >= 4 && !x.wait4(DEC_FREE, i - 4)) break;
       Decays &D = x.dec(i);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NB; ++k) {
         const float after = __shfl_down_sync(~0u, s[k], 1);
         s[k] = lane < 31 ? after : 0.f;  // behind the token, to its block's end
         if (lane == 31) D.total[b0 + k] = up[k];
@@ -495,29 +539,29 @@ __global__ void __launch_bounds__(NT, 1)
       }
       x.arrive(TOTALS);
       if (!x.wait(TOTALS, i)) break;
-      const float4 L = f4(D.total);
+      const float4 T = f4(D.total);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
+      for (int k = 0; k < NB; ++k) {
         const int tk = 32 * (b0 + k) + lane;
         float sum = s[k];
 #pragma unroll
         for (int j = 1; j < 4; ++j) {  // block b0 + k + j
           if (b0 + k + j < 4) {
             if (kOut) D.col[j - 1][tk] = d[k] * ex2(sum);
-            const int nb = k + j;  // counted from b0
-            sum += nb == 1 ? (b0 ? L.w : L.y) : nb == 2 ? L.z : L.w;
+            const int nb = b0 + k + j;
+            sum += nb == 1 ? T.y : nb == 2 ? T.z : T.w;
           }
         }
         D.w[tk] = d[k] * ex2(sum);
       }
       if (b0 == 0 && lane == 0) {
         D.before[0] = 1.f;
-        D.before[1] = ex2(L.x);
-        D.before[2] = ex2(L.x + L.y);
-        D.before[3] = ex2(L.x + L.y + L.z);
-        D.all = ex2(L.x + L.y + L.z + L.w);
+        D.before[1] = ex2(T.x);
+        D.before[2] = ex2(T.x + T.y);
+        D.before[3] = ex2(T.x + T.y + T.z);
+        D.all = ex2(T.x + T.y + T.z + T.w);
       }
-      total += L.x + L.y + L.z + L.w;
+      total += T.x + T.y + T.z + T.w;
       x.arrive(DEC + (i & 3));
     }
     if (!kOut && b0 == 0 && lane == 0 && p0 == 0) p.decays[it.item * a.H + h] = ex2(total);
@@ -535,14 +579,15 @@ __global__ void __launch_bounds__(NT, 1)
       x.arrive(DEC_FREE + (i & 3));
       const float2 f2 = make_float2(w, w);
       if (!x.wait2(F_BX, i)) break;
-      unsigned char *xt = sm + kX + (i & 1) * 16384;
+      unsigned char *xt = sm + L::X + (i & 1) * 16384, *wx = sm + L::w(i);
       auto load = [&](int k) {
         return live ? *reinterpret_cast<const uint4 *>(xt + sw128_chunk(t, k)) : make_uint4(0, 0, 0, 0);
       };
       uint4 v = load(k0);
+      if (!kOut && first && ch.count(i) < Q && !x.wait2(F_B, i)) break;
       if (first && !live) {  // rows behind the last token: x and B sum over tokens, so they must be zeros
         const uint4 z = make_uint4(0, 0, 0, 0);
-        unsigned char *bt = sm + kB + (i & 1) * 32768;
+        unsigned char *bt = sm + L::B + (i & 1) * 32768;
 #pragma unroll 1
         for (int k = 0; k < 8; ++k) {
           const uint32_t at = sw128_chunk(t, k);
@@ -551,7 +596,8 @@ __global__ void __launch_bounds__(NT, 1)
           *reinterpret_cast<uint4 *>(bt + 16384 + at) = z;
         }
       }
-      if (i >= 1 && !x.wait(DS_DONE, i - 1)) break;  // wx is read
+      // the wx that was in its place is read
+      if (i >= L::kDeep && !x.wait(DS_DONE + L::at(i), L::phase(i - L::kDeep))) break;
 #pragma unroll 2
       for (int k = k0; k < k1; ++k) {
         const uint32_t u[4] = {v.x, v.y, v.z, v.w};
@@ -564,13 +610,14 @@ __global__ void __launch_bounds__(NT, 1)
           q1[j] = take_term(y);
           q2[j] = pack_bf16x2(y.x, y.y);
         }
-        unsigned char *to = sm + kW + sw128_chunk(t, k);
+        unsigned char *to = wx + sw128_chunk(t, k);
         *reinterpret_cast<uint4 *>(to) = make_uint4(q0[0], q0[1], q0[2], q0[3]);
         *reinterpret_cast<uint4 *>(to + 16384) = make_uint4(q1[0], q1[1], q1[2], q1[3]);
         *reinterpret_cast<uint4 *>(to + 32768) = make_uint4(q2[0], q2[1], q2[2], q2[3]);
       }
       fence_proxy_async_smem();
-      x.arrive(WX_READY);
+      x.arrive(WX_READY + L::at(i));
+      if (!kOut) x.arrive(BX_FREE + (i & 1));
     }
   } else if (warp >= 16 && warp < 24) {
     // ======================= state =======================
@@ -608,33 +655,33 @@ __global__ void __launch_bounds__(NT, 1)
       x.arrive(YX_READY);
     };
     if (kOut) copy();
-    x.arrive(WX_READY);  // no dS before the first
+    for (int k = 0; k < L::kDeep; ++k) x.arrive(WX_READY + k);  // no dS before the first
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       if (!x.wait4(DEC, i)) break;
       const float keep = x.dec(i).all;
       x.arrive(DEC_FREE + (i & 3));
-      if (!x.wait(DS_DONE, i)) break;
+      if (!x.wait(DS_DONE + L::at(i), L::phase(i))) break;
       tc_fence_after();
 #pragma unroll
       for (int c = 0; c < 32; c += 8) {
         float q0[8], q1[8];
-        tmem_ld8(tl + tDS + 128 + 32 * half + c, q0);
-        tmem_ld8(tl + tDS + 64 + 32 * half + c, q1);
+        tmem_ld8(tl + L::ds(i) + 128 + 32 * half + c, q0);
+        tmem_ld8(tl + L::ds(i) + 64 + 32 * half + c, q1);
         tmem_ld_wait(q0);
         tmem_ld_touch(q1);
         float2 sum[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           sum[j] = __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), make_float2(q1[2 * j], q1[2 * j + 1]));
-        tmem_ld8(tl + tDS + 32 * half + c, q0);
+        tmem_ld8(tl + L::ds(i) + 32 * half + c, q0);
         tmem_ld_wait(q0);
 #pragma unroll
         for (int j = 0; j < 4; ++j)
           S[c / 2 + j] = __ffma2_rn(make_float2(keep, keep), S[c / 2 + j], __fadd2_rn(make_float2(q0[2 * j], q0[2 * j + 1]), sum[j]));
       }
       tc_fence_before();
-      x.arrive(WX_READY);
+      x.arrive(WX_READY + L::at(i + L::kDeep));
       if (kOut && i + 1 < n) copy();  // (DS_DONE: the products that read the copy before are done)
       if (kOut && a.page) {
         if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(ch.first(i) + ch.count(i)), p0 == 0 && t == 0))
