@@ -203,11 +203,11 @@ int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost
 // The CUDA-core kernel: two blocks of 512 threads share an SM; a token takes about
 // 0.2 us, its state pass saves the outputs' half.
 int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 16, 64, kAlign, packed); }
-// The tensor-core kernel: one block an SM; a chunk takes 2.3 us, 1.4 us in the state
+// The tensor-core kernel: one block an SM; a chunk takes 2.3 us, 1.2 us in the state
 // pass; a block's beginning and end 6 us, the two launches about 10 us.  131,072 tokens
-// of 16 heads of 128 in 9 segments: state pass 313 us, join 5 us, outputs 526 us.
+// of 16 heads of 128 in 9 segments: state pass 279 us, join 7 us, outputs 529 us.
 int tc_segment(int R, int rows, int H, int P, bool packed) {
-  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.6f, 5 * kAlign / 2, 4 * kAlign,
+  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.53f, 5 * kAlign / 2, 4 * kAlign,
                       4 * kAlign, packed);
 }
 

@@ -34,7 +34,7 @@
 // Work split: one CTA a (segment, head, 64 columns of P), 32 warps of 64 registers:
 //   warp 0       producer: TMA loads of B, x (two stages) and C
 //   warps 1, 3   decays: steps, sums of l, the factors of every role (up to four
-//                chunks ahead)
+//                chunks ahead); warps 24-27 in a state pass
 //   warp 2       issues every MMA
 //   warps 4-11   scores: two threads own row t of G, half a block of columns each;
 //                they write W to TMEM
@@ -127,8 +127,8 @@ constexpr uint32_t tG = 0, tW = 128, tDS = 192, tYi = 384, tYx = 448;  // dS: on
 // written while the products of the one before run.  And as its chunks are short against
 // the latency of their loads (2,300 cycles from a stage's release to its next tiles), x is
 // released when wx is written and B, which only the products read, on its own.  131,072
-// tokens, 16 heads of 128, 9 segments: 313 us with x and B released together and one wx.
-// Places and depth of each run:
+// tokens, 16 heads of 128, 9 segments: 279 us, against 313 with x and B released
+// together and one wx.  Places and depth of each run:
 template <bool kOut>
 struct Layout {
   static constexpr int B = kOut ? kB : 0, X = kOut ? kX : 65536, W = kOut ? kW : 98304;
@@ -337,16 +337,12 @@ __global__ void __launch_bounds__(NT, 1)
         __syncwarp();
         cloads = i + 1;
       }
-      if (i + 2 < n) {  // the chunk after the next on its way from HBM
+      // x of the chunk after the next on its way from HBM (281 us against 285 for 148 heads
+      // of 16,384 tokens; B and C are in L2 for the group's other heads: asking for them
+      // too cost 284)
+      if (i + 2 < n) {
         const int next = row_of_seq + ch.first(i + 2);
-        if (elect_one()) {
-          tma_prefetch_3d(&mx, p0, h, next);
-#pragma unroll
-          for (int c = 0; c < 16 * NK; c += 64) {
-            tma_prefetch_3d(&mb, c, g, next);
-            if (kOut) tma_prefetch_3d(&mc, c, g, next);
-          }
-        }
+        if (elect_one()) tma_prefetch_3d(&mx, p0, h, next);
         __syncwarp();
       }
     }
