@@ -13,6 +13,7 @@ using namespace kda::check;
 constexpr int kMaxMapRequests = 16384;
 constexpr int kMaxRows = INT32_MAX - 4096;      // rows and what is added to them stay 32-bit
 constexpr int kMaxChannels = 1 << 24;  // a block for each 512 of them in a grid's second dimension
+constexpr int kMaxHeads = 1 << 24;     // times 128 columns, an element's place in its row stays 32-bit
 
 size_t elem(kda_dtype_t t) { return t == KDA_DTYPE_BF16 ? 2 : 4; }
 
@@ -190,9 +191,14 @@ namespace {
 kda_status_t check_ssm_sizes(int H, int G, int N, int P, kda_dtype_t dtype) {
   if (H < 0 || G < 0) return KDA_ERR_INVALID_ARG;
   if (dtype != KDA_DTYPE_F32 && dtype != KDA_DTYPE_BF16) return KDA_ERR_DTYPE;
-  if (!supported_d(N) || !supported_d(P)) return KDA_ERR_SHAPE;
+  if (!supported_d(N) || !supported_d(P) || H > kMaxHeads) return KDA_ERR_SHAPE;
   if (H > 0 && (G == 0 || H % G != 0)) return KDA_ERR_SHAPE;
   return KDA_OK;
+}
+
+// One block for each (segment, head, slice of P), and segments of at least 128 tokens.
+bool scan_grid_fits(int R, int rows, int H) {
+  return ((int64_t)rows / 128 + 2 * (int64_t)R) <= INT32_MAX / (2 * (int64_t)(H > 0 ? H : 1));
 }
 
 // The arguments that the scan and the step share.  `rows`: of the token-major arrays.
@@ -235,6 +241,7 @@ extern "C" {
 size_t kda_ssm_scan_workspace_size(int R, int rows, int H, int G, int N, int P, kda_dtype_t dtype) {
   if (R < 0 || rows < 0 || check_ssm_sizes(H, G, N, P, dtype) != KDA_OK) return (size_t)-1;
   if (R == 0 || rows == 0 || H == 0) return 0;
+  if (rows > kMaxRows || !scan_grid_fits(R, rows, H)) return (size_t)-1;
   return kda::ssm_scan_workspace(R, rows, H, G, N, P, dtype == KDA_DTYPE_BF16);
 }
 
@@ -251,8 +258,7 @@ kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64
   if (page_size < 0 || page_size % 128 != 0) return KDA_ERR_INVALID_ARG;
   if (page_size > 0 && (table_stride < 0 || n_pages < 0)) return KDA_ERR_INVALID_ARG;
   if (R == 0 || rows == 0 || H == 0) return KDA_OK;
-  // one block for each (segment, head, slice of P), and segments of at least 128 tokens
-  if (((int64_t)rows / 128 + 2 * (int64_t)R) * H * 2 > INT32_MAX) return KDA_ERR_SHAPE;
+  if (!scan_grid_fits(R, rows, H)) return KDA_ERR_SHAPE;
   const bool snap = page_size > 0 && table_stride > 0 && n_pages > 0;
   if (snap && (!block_table || !pages)) return KDA_ERR_INVALID_ARG;
   const size_t need = kda::ssm_scan_workspace(R, rows, H, G, N, P, dtype == KDA_DTYPE_BF16);

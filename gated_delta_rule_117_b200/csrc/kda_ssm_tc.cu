@@ -759,7 +759,10 @@ __global__ void __launch_bounds__(NT, 1)
 }  // namespace
 
 bool ssm_tc_fits(const SsmArgs &a) {
-  auto row16 = [](const void *p, int64_t stride) { return ((uintptr_t)p & 15) == 0 && stride % 8 == 0; };
+  // (a tensor map's strides are below 2^40 bytes)
+  auto row16 = [](const void *p, int64_t stride) {
+    return ((uintptr_t)p & 15) == 0 && stride % 8 == 0 && stride < (int64_t(1) << 39);
+  };
   return a.bf16 && row16(a.x, a.x_stride) && row16(a.B, a.b_stride) && row16(a.C, a.c_stride) && row16(a.y, a.y_stride);
 }
 

@@ -461,7 +461,8 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
  *   A   : [H] fp32, <= 0;   D, dt_bias : [H] fp32, or NULL (zeros)
  *   state  : pool [n_slots, H, N, P] fp32, 16-byte aligned
  *   y   : [rows, H, P] dtype, y_stride
- *   H % G == 0;  N, P : each one of 16, 32, 64, 128
+ *   H % G == 0, H at most 2^24;  N, P : each one of 16, 32, 64, 128;  (rows / 128 + 2 R) H
+ *   below 2^30 (KDA_ERR_SHAPE beyond)
  * d_t A[h] <= 0 is relied on (d_t >= 0, which softplus gives).  State,
  * decays and sums are fp32; on the tensor-core path (bf16 with 16-byte aligned
  * rows) the products take bf16 operands, as noted at the kernel, and an input

@@ -340,3 +340,15 @@ def test_short_wait_limit_leaves_results_alone():
         assert kda.kda_get_device_status() == 0 and torch.equal(y, ref)
     finally:
         kda.kda_debug_set_wait_limit(0)
+
+
+def test_stride_of_a_single_row():
+    # the stride of one row is never followed, however large (a tensor map would not take it)
+    H, N, P = 2, 32, 64
+    x, dt, A, B, C, D, bias = _scan_inputs(1, H, N, P, BF, 6)
+    ref, y, far = kda.ssm_scan(x, dt, A, B, C, D, bias), torch.empty_like(x), 1 << 42
+    code = kda.kda_ssm_scan(x.data_ptr(), far, dt.data_ptr(), far, A.data_ptr(), B.data_ptr(), far, C.data_ptr(), far,
+                            D.data_ptr(), bias.data_ptr(), 1, None, 0, None, None, None, None, 0, None, 0, 0, y.data_ptr(),
+                            far, 1, 1, H, 1, N, P, 1, None, 0, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert code == 0 and rel_l2(y, _n(ref)) <= TOL[BF]

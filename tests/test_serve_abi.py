@@ -173,6 +173,17 @@ def test_sizes_that_would_not_fit_their_arithmetic():
     assert _conv_step(y_stride=1 << 48) == SHAPE and _step(c_stride=1 << 48) == SHAPE
 
 
+def test_heads_that_would_not_fit_their_arithmetic():
+    most, far = 1 << 24, 1 << 36  # a place in a row is h * 128 + c in 32 bits
+    wide = dict(G=1, N=16, P=128, R=1, x_stride=far, y_stride=far, dt_stride=far, n_slots=1)
+    assert _step(H=most + 1, **wide) == SHAPE and _scan(H=most + 1, rows=1, **wide) == SHAPE
+    assert _step(H=1 << 24, **dict(wide, R=128, n_slots=128)) == SHAPE  # and the blocks of a launch
+    bad = (1 << 64) - 1
+    assert kda.kda_ssm_scan_workspace_size(1, 1, most + 1, 1, 16, 128, 1) == bad
+    assert kda.kda_ssm_scan_workspace_size(1 << 30, (1 << 31) - 4097, 1 << 20, 1, 128, 128, 1) == bad
+    assert kda.kda_ssm_scan_workspace_size(1, (1 << 31) - 4096, 1, 1, 128, 128, 1) == bad
+
+
 def test_nothing_to_do():
     assert _conv(R=0, rows=0, x=None) == 0 and _conv(rows=0, y=None) == 0 and _conv_step(R=0) == 0
     assert _scan(R=0, rows=0, x=None) == 0 and _scan(H=0, y=None) == 0 and _step(R=0) == 0
