@@ -508,10 +508,10 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _rows(name, t, lead):
-    """Row stride of token-major `t`: `lead` leading dimensions of rows over dense rows of elements."""
-    if lead == 1 and t.is_contiguous():
-        return t.numel() if t.size(0) == 1 else t.stride(0)
+def _rows(name, t, lead, width):
+    """Row stride of token-major `t`: `lead` leading dimensions of rows over dense rows of `width` elements."""
+    if t.is_contiguous():
+        return width
     shape, stride = t.shape, t.stride()
     want = 1
     for i in range(len(shape) - 1, lead - 1, -1):
@@ -552,12 +552,22 @@ def _launch(fn, what, i, stream, args):
 
 def _good_slots(t, R, d, i32):
     """Whether t is a vector of R int32 on device d (or None)."""
-    return t is None or (t.dtype is i32 and t.dim() == 1 and t.size(0) == R and t.get_device() == d and t.is_contiguous())
+    return t is None or (t.dtype is i32 and t.shape == (R,) and t.get_device() == d and t.is_contiguous())
 
 
 def _good_vector(t, n, d, dtype):
     """The same for a parameter vector."""
-    return t is None or (t.dtype is dtype and t.dim() == 1 and t.size(0) == n and t.get_device() == d and t.is_contiguous())
+    return t is None or (t.dtype is dtype and t.shape == (n,) and t.get_device() == d and t.is_contiguous())
+
+
+def _pool_entries(t, d, dtype, *entry):
+    """Entries of a pool [n, *entry] on device d (0 without one), or -1 if t is not one."""
+    if t is None:
+        return 0
+    shape = t.shape
+    good = (len(shape) == len(entry) + 1 and shape == (shape[0], *entry) and t.dtype is dtype and t.get_device() == d and
+            t.is_contiguous())
+    return shape[0] if good else -1
 
 
 def _bad_requests(slots, ctx, cu, R):
@@ -572,13 +582,14 @@ def _bad_requests(slots, ctx, cu, R):
 def _requests(x, lead, slots, ctx, cu, d):
     """(R, rows) of a packed call, after the checks of its integer arguments."""
     i32 = _torch.int32
+    shape = x.shape
     if lead == 2:
         if cu is not None:
             raise ValueError("cu goes with [rows, ...] tensors")
-        R = x.size(0)
-        rows = R * x.size(1)
+        R = shape[0]
+        rows = R * shape[1]
     else:
-        rows = x.size(0)
+        rows = shape[0]
         R = 1 if cu is None else cu.numel() - 1
         if R < 0:
             raise ValueError("cu must hold R + 1 offsets")
@@ -596,10 +607,11 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
     tokens that the call may hold.  Returns (cu [R + 1] int32, token_slots [rows]
     int64, pages_used [1] int32)."""
     torch = _torch or _init()
-    i32, R, d = torch.int32, lens.numel(), lens.get_device()
+    i32, R, n_free, d = torch.int32, lens.numel(), free_pages.numel(), lens.get_device()
+    shape = block_table.shape
     if not (d >= 0 and _good_slots(lens, R, d, i32) and _good_slots(ctx, R, d, i32) and
-            _good_slots(free_pages, free_pages.numel(), d, i32) and block_table.dtype is i32 and block_table.dim() == 2 and
-            block_table.size(0) == R and block_table.get_device() == d and block_table.is_contiguous()):
+            _good_slots(free_pages, n_free, d, i32) and block_table.dtype is i32 and len(shape) == 2 and shape[0] == R and
+            block_table.get_device() == d and block_table.is_contiguous()):
         _typed(i32, "lens ctx free_pages block_table", lens, ctx, free_pages, block_table)
         _dense("lens ctx free_pages block_table", lens, ctx, free_pages, block_table)
         _on(lens, ctx, free_pages, block_table)
@@ -621,8 +633,8 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
         _dense("cu token_slots pages_used", cu, token_slots, pages_used)
         _on(lens, cu, token_slots, pages_used)
     _launch(load_library().kda_block_map, "kda_block_map", d, stream,
-            (lens.data_ptr(), _at(ctx), free_pages.data_ptr(), free_pages.numel(), block_table.data_ptr(),
-             block_table.size(1), page_size, cu.data_ptr(), token_slots.data_ptr(), pages_used.data_ptr(), R, rows))
+            (lens.data_ptr(), _at(ctx), free_pages.data_ptr(), n_free, block_table.data_ptr(), shape[1], page_size,
+             cu.data_ptr(), token_slots.data_ptr(), pages_used.data_ptr(), R, rows))
     return cu, token_slots, pages_used
 
 
@@ -646,22 +658,21 @@ def _output(x, y, lead, width, stream):
     _typed(x.dtype, "y", y)
     _shaped("y", y, x.shape)
     _on(x, y)
-    return y, _rows("y", y, lead)
+    return y, _rows("y", y, lead, width)
 
 
 def _conv_weights(x, w, bias, state, C, d):
-    """The number of taps, after the checks of weights and pool."""
-    t = x.dtype
-    K = w.size(1) if w.dim() == 2 else 0
-    if not (d >= 0 and K > 0 and w.dtype is t and w.size(0) == C and w.get_device() == d and w.is_contiguous() and
-            _good_vector(bias, C, d, t) and
-            (state is None or (state.dtype is t and state.dim() == 3 and state.size(1) == K - 1 and state.size(2) == C and
-                               state.get_device() == d and state.is_contiguous()))):
+    """(taps, entries of the pool), after the checks of weights and pool."""
+    t, shape = x.dtype, w.shape
+    K = shape[1] if len(shape) == 2 else 0
+    n = _pool_entries(state, d, t, K - 1, C)
+    if not (d >= 0 and K > 0 and n >= 0 and w.dtype is t and shape[0] == C and w.get_device() == d and w.is_contiguous() and
+            _good_vector(bias, C, d, t)):
         _typed(t, "w bias state", w, bias, state)
         _dense("w bias state", w, bias, state)
         _on(x, w, bias, state)
         raise ValueError("w must be [C, K], bias [C], state [n_slots, K - 1, C]")
-    return K
+    return K, n
 
 
 def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, silu=True, head_dim=0, l2norm=False,
@@ -676,8 +687,8 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
     lead = x.dim() - 1
     if lead not in (1, 2):
         raise ValueError("x must be [rows, C] or [B, T, C]")
-    C, d = x.size(lead), x.get_device()
-    K = _conv_weights(x, w, bias, state, C, d)
+    C, d = x.shape[lead], x.get_device()
+    K, n_slots = _conv_weights(x, w, bias, state, C, d)
     R, rows = _requests(x, lead, slots, ctx, cu, d)
     if not head_major:
         y, ys = _output(x, y, lead, C, stream)
@@ -694,7 +705,7 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
             _on(x, y)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0) | (KDA_CONV_HEAD_MAJOR if head_major else 0)
     _launch(load_library().kda_short_conv, "kda_short_conv", d, stream,
-            (x.data_ptr(), _rows("x", x, lead), w.data_ptr(), _at(bias), _at(state), 0 if state is None else state.size(0),
+            (x.data_ptr(), _rows("x", x, lead, C), w.data_ptr(), _at(bias), _at(state), n_slots,
              _at(slots), _at(ctx), _at(cu), y.data_ptr(), ys, R, rows, C, K, head_dim, code, flags, eps))
     return y
 
@@ -707,30 +718,31 @@ def short_conv_step(x, w, state, bias=None, *, slots=None, silu=True, head_dim=0
     code = _dtype_code(x)
     if x.dim() != 2:
         raise ValueError("x must be [R, C]")
-    R, C, d = x.size(0), x.size(1), x.get_device()
-    K = _conv_weights(x, w, bias, state, C, d)
+    R, C = x.shape
+    d = x.get_device()
+    K, n_slots = _conv_weights(x, w, bias, state, C, d)
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
     y, ys = _output(x, y, 1, C, stream)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0)
     _launch(load_library().kda_short_conv_step, "kda_short_conv_step", d, stream,
-            (x.data_ptr(), _rows("x", x, 1), w.data_ptr(), _at(bias), state.data_ptr(), state.size(0), _at(slots),
+            (x.data_ptr(), _rows("x", x, 1, C), w.data_ptr(), _at(bias), _at(state), n_slots, _at(slots),
              y.data_ptr(), ys, R, C, K, head_dim, code, flags, eps))
     return y
 
 
 def _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d):
-    """(H, G, N, P, row strides) after the checks of shapes, types and layouts."""
+    """(H, G, N, P, entries of the pool, row strides) after the checks of shapes, types and layouts."""
     f32, t = _torch.float32, x.dtype
-    H, P, G, N = x.size(lead), x.size(lead + 1), B.size(-2), B.size(-1)
     shape, bshape = x.shape, B.shape
-    if not (d >= 0 and dt.dtype is t and B.dtype is t and C.dtype is t and dt.shape == shape[:-1] and
-            bshape[:-2] == shape[:-2] and C.shape == bshape and dt.get_device() == d and B.get_device() == d and
+    H, P, G, N = shape[lead], shape[lead + 1], bshape[lead], bshape[lead + 1]
+    rows = shape[:lead]
+    n = _pool_entries(state, d, f32, H, N, P)
+    if not (d >= 0 and n >= 0 and dt.dtype is t and B.dtype is t and C.dtype is t and dt.shape == (*rows, H) and
+            bshape == (*rows, G, N) and C.shape == bshape and dt.get_device() == d and B.get_device() == d and
             C.get_device() == d and _good_vector(A, H, d, f32) and _good_vector(D, H, d, f32) and
-            _good_vector(dt_bias, H, d, f32) and
-            (state is None or (state.dtype is f32 and state.dim() == 4 and state.size(1) == H and state.size(2) == N and
-                               state.size(3) == P and state.get_device() == d and state.is_contiguous()))):
+            _good_vector(dt_bias, H, d, f32)):
         _typed(t, "dt B C", dt, B, C)
         _typed(f32, "A D dt_bias state", A, D, dt_bias, state)
         _dense("A D dt_bias state", A, D, dt_bias, state)
@@ -739,7 +751,8 @@ def _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d):
         _shaped("B", B, shape[:-2] + bshape[-2:])
         _shaped("C", C, bshape)
         raise ValueError("A, D and dt_bias must be [H], state [n_slots, H, N, P]")
-    return H, G, N, P, _rows("x", x, lead), _rows("dt", dt, lead), _rows("B", B, lead), _rows("C", C, lead)
+    return (H, G, N, P, n, _rows("x", x, lead, H * P), _rows("dt", dt, lead, H), _rows("B", B, lead, G * N),
+            _rows("C", C, lead, G * N))
 
 
 def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None, slots=None, ctx=None, cu=None,
@@ -757,7 +770,7 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
     if lead not in (1, 2) or B.dim() != lead + 2:
         raise ValueError("x must be [rows, H, P] or [B, T, H, P], B and C [.., G, N]")
     d = x.get_device()
-    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d)
+    H, G, N, P, n_slots, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, lead, d)
     R, rows = _requests(x, lead, slots, ctx, cu, d)
     width = n_pages = 0
     if page_size:
@@ -788,7 +801,7 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
         wbytes = workspace.numel() * workspace.element_size()
     _launch(lib.kda_ssm_scan, "kda_ssm_scan", d, stream,
             (x.data_ptr(), xs, dt.data_ptr(), ds, A.data_ptr(), B.data_ptr(), bs, C.data_ptr(), cs, _at(D), _at(dt_bias),
-             1 if softplus else 0, _at(state), 0 if state is None else state.size(0), _at(slots), _at(ctx), _at(cu),
+             1 if softplus else 0, _at(state), n_slots, _at(slots), _at(ctx), _at(cu),
              _at(block_table), width, _at(pages), n_pages, page_size, y.data_ptr(), ys, R, rows, H, G, N, P, code,
              _at(workspace), wbytes))
     return y
@@ -801,13 +814,13 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, softplus=True, slot
     code = _dtype_code(x)
     if x.dim() != 3 or B.dim() != 3:
         raise ValueError("x must be [R, H, P], B and C [R, G, N]")
-    R, d = x.size(0), x.get_device()
-    H, G, N, P, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, 1, d)
+    R, d = x.shape[0], x.get_device()
+    H, G, N, P, n_slots, xs, ds, bs, cs = _ssm_args(x, dt, A, B, C, D, dt_bias, state, 1, d)
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
     y, ys = _output(x, y, 1, H * P, stream)
     _launch(load_library().kda_ssm_step, "kda_ssm_step", d, stream,
             (x.data_ptr(), xs, dt.data_ptr(), ds, A.data_ptr(), B.data_ptr(), bs, C.data_ptr(), cs, _at(D), _at(dt_bias),
-             1 if softplus else 0, state.data_ptr(), state.size(0), _at(slots), y.data_ptr(), ys, R, H, G, N, P, code))
+             1 if softplus else 0, _at(state), n_slots, _at(slots), y.data_ptr(), ys, R, H, G, N, P, code))
     return y
