@@ -1,6 +1,6 @@
 // Selective state space scan of packed prompts (include/kda.h, kda_ssm_scan):
-// the CUDA-core kernel (fp32 and any size), and the segment bookkeeping that
-// every scan kernel shares.
+// the CUDA-core kernel (fp32, rows of any alignment, many sequences of a few
+// tokens), and the segment bookkeeping that every scan kernel shares.
 //
 //     S_t = exp(d_t A) S_{t-1} + d_t B_t x_t^T,    y_t = S_t^T C_t + D x_t.
 //
@@ -248,9 +248,28 @@ size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16)
   return most;
 }
 
+// Whether the CUDA-core kernel should take a call that fits both: many sequences of a few
+// tokens, as its blocks are small and several share an SM.  In us, fitted to 1 to 256
+// sequences of 1 to 64 tokens, 3 to 32 heads of 16 x 16 to 128 x 128: a state's way in and out
+// and a token's work over the machine, the chain of the longest sequence's tokens, and waves of
+// the other kernel's blocks.  256 x 32 heads of 128 x 64, one token each: 151 us against 322;
+// 16 tokens: 447 against 532; 64 tokens: 1,384 against 501.  The longest of a packed call is
+// not known: what is lost if one sequence has all the rows must not exceed what is gained
+// if it has twice the mean.
+static bool tokens_are_few(const SsmArgs &a) {
+  const double states = (double)a.q.R * a.H, np = (double)a.N * a.P, mean = (double)a.q.rows / a.q.R;
+  auto simt = [&](double longest) {
+    return 4 + states * np * (2.2e-6 + 0.3e-6 * mean) + longest * (0.12 + 0.0028 * a.N * (a.P > 64 ? 1.5 : 1));
+  };
+  const double waves = fmax(1, states * ((a.P + 63) / 64) / 148);
+  const double tc = waves * (mean <= kShort ? 3.8 + 0.015 * a.N + mean * (0.12 + 0.001 * a.N)
+                                            : 6 + 0.02 * a.N + 2.3 * floor((mean - 1) / kAlign));
+  return a.q.cu ? simt(fmin(a.q.rows, 2 * mean)) * simt(a.q.rows) < tc * tc : simt(mean) < tc;
+}
+
 cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st) {
   const bool packed = a.q.cu != nullptr;
-  if (ssm_tc_fits(a)) return launch_ssm_tc(a, tc_segment(a.q.R, a.q.rows, a.H, a.P, packed), st);
+  if (ssm_tc_fits(a) && !tokens_are_few(a)) return launch_ssm_tc(a, tc_segment(a.q.R, a.q.rows, a.H, a.P, packed), st);
   const int seg = simt_segment(a.q.R, a.q.rows, a.H, packed);
 #define KDA_SSM_CASE(NN, PP)    \
   if (a.N == NN && a.P == PP)   \

@@ -247,6 +247,85 @@ __device__ __forceinline__ uint32_t take_term(float2 &v) {
   return h;
 }
 
+// An item of at most kShort tokens: token by token in fp32, without the tensor cores.  A
+// thread owns one column of NK rows, so state moves in whole lines, and the 16 row groups'
+// shares of y are added at the end: the loop over tokens has no barrier.  One wave, N = 128: 5.6 us
+// for one token, 0.25 more for each; the chunk form (barriers, tensor memory, three products
+// one after another) takes 9.6 us for any number up to 128.
+template <int NK>
+__device__ __forceinline__ void short_item(const TcArgs &p, const Item &it, unsigned char *sm, int h, int g, int p0) {
+  constexpr int N = 16 * NK;
+  const SsmArgs &a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, c = 32 * (tid >> 5 & 1) + lane, group = tid >> 6;
+  const int len = it.end - it.begin;
+  float *sB = reinterpret_cast<float *>(sm), *sC = sB + kShort * N, *sx = sC + kShort * N, *part = sx + kShort * PC;
+  float *sd = part + kShort * 16 * PC, *sa = sd + kShort;
+  static_assert((kShort * (2 * N + 17 * PC + 2)) * 4 <= kSmemBytes - 1024, "shared memory of a short item");
+  const bool mine = p0 + c < a.P;
+  const int at = group * NK * a.P + p0 + c;  // of this thread's first row
+  const int64_t np = (int64_t)N * a.P;
+  const float *from = nullptr;
+  if (p.seg != 0) from = p.ws + (it.item * a.H + h) * np;
+  else if (a.state && it.s.ctx > 0) from = a.state + ((int64_t)it.s.slot * a.H + h) * np;
+  float S[NK];
+#pragma unroll
+  for (int j = 0; j < NK; ++j) S[j] = from && mine ? from[at + j * a.P] : 0.f;
+  auto save = [&](float *to) {
+#pragma unroll
+    for (int j = 0; j < NK; ++j)
+      if (mine) to[at + j * a.P] = S[j];
+  };
+  const int64_t row0 = (int64_t)it.s.start + it.begin;
+  auto spread = [](float *to, uint4 v) {  // eight bf16
+    const float2 f[4] = {unpack(v.x), unpack(v.y), unpack(v.z), unpack(v.w)};
+    *reinterpret_cast<float4 *>(to) = make_float4(f[0].x, f[0].y, f[1].x, f[1].y);
+    *reinterpret_cast<float4 *>(to + 4) = make_float4(f[2].x, f[2].y, f[3].x, f[3].y);
+  };
+  auto eight = [](const void *base, int64_t i) { return *reinterpret_cast<const uint4 *>((const __nv_bfloat16 *)base + i); };
+  for (int e = tid; e < len * 2 * NK; e += NT) {
+    const int t = e / (2 * NK), k = e % (2 * NK) * 8;
+    const uint4 b = eight(a.B, (row0 + t) * a.b_stride + g * N + k), q = eight(a.C, (row0 + t) * a.c_stride + g * N + k);
+    spread(sB + t * N + k, b);
+    spread(sC + t * N + k, q);
+  }
+  for (int e = tid; e < len * (PC / 8); e += NT) {
+    const int t = e / (PC / 8), k = e % (PC / 8) * 8;
+    spread(sx + t * PC + k, p0 + k < a.P ? eight(a.x, (row0 + t) * a.x_stride + h * a.P + p0 + k) : make_uint4(0, 0, 0, 0));
+  }
+  if (tid < len) {
+    const float d = time_step<__nv_bfloat16>(a, row0 + tid, h);
+    sd[tid] = d;
+    sa[tid] = expf(d * a.A[h]);
+  }
+  __syncthreads();
+#pragma unroll 2
+  for (int t = 0; t < len; ++t) {
+    const float keep = sa[t], dx = sd[t] * sx[t * PC + c], *b = sB + t * N + group * NK, *q = sC + t * N + group * NK;
+    float y = 0.f;
+#pragma unroll
+    for (int j = 0; j < NK; ++j) {
+      S[j] = fmaf(b[j], dx, keep * S[j]);
+      y = fmaf(q[j], S[j], y);
+    }
+    part[(t * 16 + group) * PC + c] = y;
+    if (a.page)
+      if (float *to = snapshot(a, it.r, h, (uint32_t)it.s.ctx + (uint32_t)(it.begin + t + 1), p0 == 0 && tid == 0)) save(to);
+  }
+  if (a.state && it.index == it.count - 1) save(a.state + ((int64_t)it.s.slot * a.H + h) * np);
+  __syncthreads();
+  const float skip = a.D ? a.D[h] : 0.f;
+  for (int e = tid; e < len * (PC / 2); e += NT) {
+    const int t = e / (PC / 2), k = e % (PC / 2) * 2;
+    if (p0 + k >= a.P) continue;
+    const float2 xv = *reinterpret_cast<const float2 *>(sx + t * PC + k);
+    float2 y = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) y = __fadd2_rn(y, *reinterpret_cast<const float2 *>(part + (t * 16 + i) * PC + k));
+    y = __ffma2_rn(make_float2(skip, skip), xv, y);
+    *reinterpret_cast<uint32_t *>((__nv_bfloat16 *)a.y + (row0 + t) * a.y_stride + h * a.P + p0 + k) = pack_bf16x2(y.x, y.y);
+  }
+}
+
 // kOut: the run that writes y, snapshots and final states; else the state pass,
 // which leaves each segment's S~ and decay in the workspace.
 // NK: K steps over N (N / 16).
@@ -265,8 +344,13 @@ __global__ void __launch_bounds__(NT, 1)
   Item it;
   if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, reinterpret_cast<int *>(sm + L::W), it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
+  const int g = h / (a.H / a.G);
+  if (kOut && it.end - it.begin <= kShort) {
+    short_item<NK>(p, it, sm, h, g, p0);
+    return;
+  }
   const Chunks ch(it);
-  const int n = ch.n, g = h / (a.H / a.G);
+  const int n = ch.n;
 
   Cta x;
   x.sm = sm;
