@@ -24,7 +24,7 @@
 namespace kda {
 namespace {
 
-constexpr int TB = 16;  // tokens staged at a time
+constexpr int TB = kSimtAlign;  // tokens staged at a time
 
 template <int N, int P, typename T, bool kOut>
 __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, float *ws, float *decays) {
@@ -37,7 +37,7 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
   const bool tell = kOut && h == 0 && tid == 0;
   Item it;
   __shared__ int scratch[kMaxRanked + 1];
-  if (!item_of(a.q, blockIdx.x / a.H, seg, tell, scratch, it)) return;
+  if (!item_of(a.q, blockIdx.x / a.H, seg, kSimtAlign, tell, scratch, it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const int g = h / (a.H / a.G);
   float2 S[J][2];  // rows 16 j + 4 quarter + 0 .. 3
@@ -132,7 +132,7 @@ __global__ void __launch_bounds__(4 * P) ssm_scan_kernel(SsmArgs a, int seg, flo
 // Entering states of every segment of a sequence, in place of what the segments
 // add to a zero state: S(0) from the pool, S(i + 1) = a_i S(i) + S~_i.
 constexpr int kJoinThreads = 128, kAhead = 8;
-__global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a, int seg, float4 *ws,
+__global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a, int seg, int align, float4 *ws,
                                                                       const float *decays) {
   const int r = blockIdx.x / a.H, h = blockIdx.x % a.H;
   const int n4 = a.N * a.P / 4, e = blockIdx.y * kJoinThreads + threadIdx.x;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a,
   const int len = s.end - s.start;
   if (e >= n4 || !s.ok || len == 0) return;
   const int64_t base = seg_base(a.q, r, seg);
-  const int count = (int)(((int64_t)(s.ctx % kAlign) + len + seg - 1) / seg);
+  const int count = (int)(((int64_t)(s.ctx % align) + len + seg - 1) / seg);
   float4 S = make_float4(0.f, 0.f, 0.f, 0.f);
   if (a.state && s.ctx > 0)
     S = reinterpret_cast<const float4 *>(a.state)[((int64_t)s.slot * a.H + h) * n4 + e];
@@ -169,29 +169,31 @@ __global__ void __launch_bounds__(kJoinThreads) segment_states_kernel(SsmArgs a,
   }
 }
 
-// Segment length (a multiple of kAlign), or 0 for whole sequences: the choice whose
-// blocks' waves over the SMs cost least.
-//   blocks : blocks that an item of `H` heads makes
-//   resident : blocks that run at once
-//   state_cost : time of a state pass over a chunk, in output passes
-//   block_cost : time that a block takes to begin and to end, in tokens
-//   launch_cost : time of the two more launches, in tokens of the output pass
-//   shortest : tokens that a segment has at least
-// Whole sequences run as long as the longest of them; packed ones (whose lengths
-// the host does not see) are taken to hold one of twice the mean.
-int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost, int block_cost, int launch_cost, int shortest,
-                 bool packed) {
-  auto waves = [&](double items) { return ceil(items * blocks / resident); };
-  const double mean = (double)rows / R;
-  const double most = packed && R > 1 ? fmin((double)rows, 2 * mean) : mean;
-  // blocks of unequal length fill the machine as they come: the waves' total, or the longest block
-  double best = packed && R > 1 ? fmax(most, (mean + block_cost) * R * blocks / resident) : waves(R) * (mean + block_cost);
+// Segment lengths: those whose blocks cost least, or 0 for whole sequences.  Whole sequences
+// run as long as the longest of them; packed ones (whose lengths the host does not see) are
+// taken to hold one of twice the mean.
+
+// The CUDA-core kernel, in tokens of a block that runs alone (0.16 us for a state of 16 x 16,
+// 0.47 for 128 x 64, 0.69 for 128 x 128).  A pass takes its longest block and 16 tokens to begin and
+// end, or, where blocks share an SM, their tokens (and 7 each for the state's way in and
+// out) over its speed: that of 6.2 lone blocks of 16 x 16, of 0.92 of 128 x 128, a power of N P
+// between them.  A state pass takes 0.6 of an output pass, the two more launches 20
+// tokens, the join one a segment.  2 x 300 tokens of 4 heads of 128 x 64: 138 us whole, 96 in
+// segments of 128, 29 in segments of 16; 4,000 tokens of 4 heads of 64 x 64: 1,092 whole, 66 by 128,
+// 55 by 64, 72 by 16.
+int simt_segment(int R, int rows, int H, int N, int P, bool packed) {
+  packed = packed && R > 1;
+  const double mean = (double)rows / R, most = packed ? fmin((double)rows, 2 * mean) : mean;
+  const double speed = 6.2 * pow(256.0 / (N * P), 0.46);
+  auto pass = [&](double items, double len, double longest) {
+    return fmax(longest + 16, ceil(items * H / 148) * (len + 7) / speed);
+  };
+  double best = pass(R, mean, most);
   int seg = 0;
-  for (int k = 2; k <= 64; ++k) {
-    const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
-    if (len < shortest) break;
-    const double items = packed && R > 1 ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
-    const double cost = waves(items) * (len + block_cost) * (1 + state_cost) + launch_cost;
+  for (int k = 2, len = 0; k <= 256 && len != kSimtAlign; ++k) {
+    len = ((int)(mean / k) / kSimtAlign + 1) * kSimtAlign;
+    const double items = packed ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
+    const double cost = 1.6 * pass(items, len, len) + 20 + most / len;
     if (cost < best) {
       best = cost;
       seg = len;
@@ -200,15 +202,27 @@ int plan_segment(int R, int rows, int64_t blocks, int resident, float state_cost
   return seg;
 }
 
-// The CUDA-core kernel: two blocks of 512 threads share an SM; a token takes about
-// 0.2 us, its state pass saves the outputs' half.
-int simt_segment(int R, int rows, int H, bool packed) { return plan_segment(R, rows, H, 296, 0.6f, 16, 64, kAlign, packed); }
-// The tensor-core kernel: one block an SM; a chunk takes 2.3 us, 1.2 us in the state
-// pass; a block's beginning and end 6 us, the two launches about 10 us.  131,072 tokens
-// of 16 heads of 128 in 9 segments: state pass 279 us, join 7 us, outputs 529 us.
+// The tensor-core kernel, in tokens of an output pass: one block an SM; a chunk takes 2.3 us,
+// 1.2 us in the state pass; a block's beginning and end 6 us, the two launches about 10 us.
+// 131,072 tokens of 16 heads of 128 in 9 segments: state pass 279 us, join 7 us, outputs 529 us.
 int tc_segment(int R, int rows, int H, int P, bool packed) {
-  return plan_segment(R, rows, (int64_t)H * ((P + 63) / 64), 148, 0.53f, 5 * kAlign / 2, 4 * kAlign,
-                      4 * kAlign, packed);
+  packed = packed && R > 1;
+  const double blocks = (double)H * ((P + 63) / 64) / 148, begin = 2.5 * kAlign;
+  const double mean = (double)rows / R, most = packed ? fmin((double)rows, 2 * mean) : mean;
+  // blocks of unequal length fill the machine as they come: the waves' total, or the longest block
+  double best = packed ? fmax(most, (mean + begin) * R * blocks) : ceil(R * blocks) * (mean + begin);
+  int seg = 0;
+  for (int k = 2; k <= 64; ++k) {
+    const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
+    if (len < 4 * kAlign) break;
+    const double items = packed ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
+    const double cost = ceil(items * blocks) * (len + begin) * 1.53 + 4 * kAlign;
+    if (cost < best) {
+      best = cost;
+      seg = len;
+    }
+  }
+  return seg;
 }
 
 template <int N, int P, typename T>
@@ -219,7 +233,7 @@ cudaError_t launch_t(const SsmArgs &a, int seg, cudaStream_t st) {
   if (seg) {
     ssm_scan_kernel<N, P, T, false><<<grid, 4 * P, 0, st>>>(a, seg, ws, dec);
     cudaError_t e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_segment_states(a, seg, st);
+    if (e == cudaSuccess) e = launch_segment_states(a, seg, kSimtAlign, st);
     if (e != cudaSuccess) return e;
   }
   ssm_scan_kernel<N, P, T, true><<<grid, 4 * P, 0, st>>>(a, seg, ws, dec);
@@ -228,9 +242,9 @@ cudaError_t launch_t(const SsmArgs &a, int seg, cudaStream_t st) {
 
 }  // namespace
 
-cudaError_t launch_segment_states(const SsmArgs &a, int seg, cudaStream_t st) {
+cudaError_t launch_segment_states(const SsmArgs &a, int seg, int align, cudaStream_t st) {
   const dim3 grid((unsigned)((int64_t)a.q.R * a.H), (a.N * a.P / 4 + kJoinThreads - 1) / kJoinThreads);
-  segment_states_kernel<<<grid, kJoinThreads, 0, st>>>(a, seg, (float4 *)seg_states(a),
+  segment_states_kernel<<<grid, kJoinThreads, 0, st>>>(a, seg, align, (float4 *)seg_states(a),
                                                        seg_decays(a, scan_items(a.q.R, a.q.rows, seg)));
   return cudaGetLastError();
 }
@@ -241,7 +255,7 @@ size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16)
   size_t most = 0;
   for (int packed = 0; packed < 2; ++packed)
     for (int tc = 0; tc <= (bf16 ? 1 : 0); ++tc) {
-      const int seg = tc ? tc_segment(R, rows, H, P, packed) : simt_segment(R, rows, H, packed);
+      const int seg = tc ? tc_segment(R, rows, H, P, packed) : simt_segment(R, rows, H, N, P, packed);
       const size_t need = seg ? seg_workspace(scan_items(R, rows, seg), H, N, P) : 0;
       most = need > most ? need : most;
     }
@@ -270,7 +284,7 @@ static bool tokens_are_few(const SsmArgs &a) {
 cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t st) {
   const bool packed = a.q.cu != nullptr;
   if (ssm_tc_fits(a) && !tokens_are_few(a)) return launch_ssm_tc(a, tc_segment(a.q.R, a.q.rows, a.H, a.P, packed), st);
-  const int seg = simt_segment(a.q.R, a.q.rows, a.H, packed);
+  const int seg = simt_segment(a.q.R, a.q.rows, a.H, a.N, a.P, packed);
 #define KDA_SSM_CASE(NN, PP)    \
   if (a.N == NN && a.P == PP)   \
     return a.bf16 ? launch_t<NN, PP, __nv_bfloat16>(a, seg, st) : launch_t<NN, PP, float>(a, seg, st);

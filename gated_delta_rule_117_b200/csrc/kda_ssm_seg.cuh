@@ -2,20 +2,21 @@
 // same for every scan kernel.
 //
 // Cuts lie at multiples of `seg` tokens on an axis that starts at the last
-// multiple of kAlign before a sequence's first token (counted with ctx), so
-// chunks of kAlign tokens inside a segment end where snapshots may be wanted.
+// multiple of `align` before a sequence's first token (counted with ctx), so
+// chunks of `align` tokens inside a segment end where snapshots may be wanted.
 // Work items are numbered without the lengths: sequence r's begin at
 //     base(r) = floor(cu[r] / seg) + 2 r,
-// which leaves room for its ceil((ctx % kAlign + len) / seg) segments, as that is
+// which leaves room for its ceil((ctx % align + len) / seg) segments, as that is
 // at most 1 + ceil(len / seg) <= floor(cu[r + 1] / seg) - floor(cu[r] / seg) + 2
-// while kAlign <= seg.  Items between a sequence's last segment and the next
+// while align <= seg.  Items between a sequence's last segment and the next
 // base have no work.
 #pragma once
 #include "kda_serve.cuh"
 
 namespace kda {
 
-constexpr int kAlign = 128;
+constexpr int kAlign = 128;     // `align` of the tensor-core kernel: its chunks
+constexpr int kSimtAlign = 16;  // of the CUDA-core kernel: the tokens that it stages at a time
 
 // Items of a call (seg 0: one for each sequence).
 inline int64_t scan_items(int R, int rows, int seg) { return seg == 0 ? R : (int64_t)rows / seg + 2 * (int64_t)R; }
@@ -60,7 +61,7 @@ __device__ __forceinline__ int sequence_of_rank(const Requests &q, int item, int
 
 // The block's work item; false: none.  Every thread of the block must call it;
 // `scratch` as above.
-__device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, bool tell, int *scratch, Item &it) {
+__device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, int align, bool tell, int *scratch, Item &it) {
   if (seg == 0) {
     it.r = q.cu && q.R > 1 && q.R <= kMaxRanked ? sequence_of_rank(q, item, scratch) : item;
   } else {
@@ -71,7 +72,7 @@ __device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, bo
   it.item = item;
   const int len = it.s.end - it.s.start;
   if (!it.s.ok || len == 0) return false;
-  const int off = it.s.ctx % kAlign;
+  const int off = it.s.ctx % align;
   it.index = seg == 0 ? 0 : item - seg_base(q, it.r, seg);
   it.count = seg == 0 ? 1 : (int)(((int64_t)off + len + seg - 1) / seg);
   if (it.index < 0 || it.index >= it.count) return false;
@@ -88,7 +89,7 @@ inline float *seg_decays(const SsmArgs &a, int64_t items) { return seg_states(a)
 inline size_t seg_workspace(int64_t items, int H, int N, int P) {
   return (size_t)((items * H * ((int64_t)N * P + 1) * 4 + 15) & ~(int64_t)15);
 }
-cudaError_t launch_segment_states(const SsmArgs &a, int seg, cudaStream_t st);
+cudaError_t launch_segment_states(const SsmArgs &a, int seg, int align, cudaStream_t st);
 
 // Tokens up to which the tensor-core kernel runs an item token by token.
 constexpr int kShort = 16;

@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(NT, 1)
   const bool tell = kOut && p0 == 0 && h == 0 && tid == 0;
   unsigned char *sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   Item it;
-  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, tell, reinterpret_cast<int *>(sm + L::W), it)) return;
+  if (!item_of(a.q, blockIdx.x / (slices * a.H), p.seg, kAlign, tell, reinterpret_cast<int *>(sm + L::W), it)) return;
   if (!kOut && it.index == it.count - 1) return;  // nothing follows it
   const int g = h / (a.H / a.G);
   if (kOut && it.end - it.begin <= kShort) {
@@ -862,7 +862,7 @@ cudaError_t launch_nk(const CUtensorMap &mx, const CUtensorMap &mb, const CUtens
   if (p.seg) {
     ssm_tc_kernel<false, NK><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);
     e = cudaGetLastError();
-    if (e == cudaSuccess) e = launch_segment_states(p.a, p.seg, st);
+    if (e == cudaSuccess) e = launch_segment_states(p.a, p.seg, kAlign, st);
     if (e != cudaSuccess) return e;
   }
   ssm_tc_kernel<true, NK><<<grid, NT, kSmemBytes, st>>>(mx, mb, mc, my, p);

@@ -156,6 +156,14 @@ def test_segments_of_a_long_prompt(dtype):
     _check([1500, 3, 600], 2, 2, 16, 64, dtype, ctx=[77, 0, 300], slots=[1, 0, 4])
 
 
+@pytest.mark.parametrize("lens,over", [([70, 200], dict(ctx=[5, 130], page=128)), ([33], {}), ([49, 0, 1, 700], dict(ctx=[15, 0, 16, 17])),
+                                       ([130, 130], dict(packed=False, ctx=[127, 0], page=128)), ([1, 2, 400, 3], dict(slots=[0, -1, 2, 3]))])
+@pytest.mark.parametrize("N,P", [(16, 16), (64, 32), (128, 128)])
+def test_short_segments_in_fp32(lens, over, N, P):
+    # the CUDA-core kernel's segments may be as short as 16 tokens
+    _check(lens, 2, 1, N, P, F32, **over)
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 @pytest.mark.parametrize("page", [128, 256])
 def test_snapshots(page, dtype):
