@@ -9,11 +9,13 @@
 //     Yx = C S        128 x 64 x N       what the entering state gives
 //     dS = B^T wx     128 x 64 x 128     (wx = d 2^{L_127 - L} x, in three bf16 terms)
 //     Yi = W x        128 x 64 x 128     (W = G masked and decayed, A operand in TMEM)
-// Every exponent is a sum of l over consecutive tokens, formed from sums inside
-// blocks of 32 tokens and whole-block totals, never as a difference of long
-// sums: decays as small as those of one token keep their relative accuracy, and
-// none overflows (l <= 0).  Below the diagonal blocks the decay factors into a
-// row and a column part, so exponentials are taken for the diagonal blocks only.
+// Every exponent is a sum of l over exactly the tokens that it spans, all of one sign,
+// never a difference of two sums: decays as small as those of one token keep their
+// relative accuracy beside a step that wipes the state out (1e4 and more, where a
+// difference of sums loses them), and l = -inf gives 0, not NaN.  Below the
+// diagonal blocks of 32 tokens the decay factors into a row and a column part, sums over
+// a block's end or beginning and whole blocks between, so exponentials are taken for the
+// diagonal blocks only; there a thread adds l up from its row backwards.
 //
 // Rounding.  The state lives in fp32 registers; what is added to it is split into
 // three bf16 terms (24 bits), so the state keeps fp32 accuracy: one bf16 would be off
@@ -81,13 +83,14 @@ constexpr int kW = 131072;         // wx terms, 3 x 16 KB
 constexpr int kS = 180224;         // S as bf16 [n][p], 16 KB
 constexpr int kY = 196608;         // y, 16 KB
 constexpr int kDec = 212992;       // [4] Decays
-constexpr int kBarOff = 225536;
-constexpr int kMisc = 225792;      // Misc
-constexpr int kSmemBytes = 225920 + 1024;
+constexpr int kBarOff = 227584;
+constexpr int kMisc = 227840;      // Misc
+constexpr int kSmemBytes = 227968 + 1024;
 
 struct Decays {
   float d[Q];        // step (0 behind the last token)
   float pre[Q];      // sum of l from the token's block's first token to the token
+  float mid[Q];      // the same from the token's half block's first token
   float w[Q];        // d 2^(sum behind the token to the chunk's end)
   float col[3][Q];   // d 2^(sum behind the token to the start of the block i + 1, i + 2, i + 3 of its own i)
   float total[4];    // sum of l of each block
@@ -508,6 +511,8 @@ __global__ void __launch_bounds__(NT, 1)
     // ======================= scores =======================
     const int b = warp & 3, half = (warp - 4) >> 2;  // this warp's rows are block b, its columns a half of each block
     const uint32_t tg = tl + tG + 16 * half, tw = tl + tW + 8 * half;
+    const float A2 = a.A[h] * 1.4426950408889634f;
+    const int row = lane - 16 * half;  // the diagonal block's columns of this half up to the row
     {  // tokens behind this warp's block: zeros, once
       const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll 1
@@ -541,12 +546,22 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_ld16(tg + 32 * (c + 1), v);
         tmem_st8(tw + 16 * c, w);
       }
-      float2 e[8];  // the diagonal block's factors, formed while its scores arrive
+      // the diagonal block's factors, formed while its scores arrive: from the half's last column
+      // back, with the sum of l from behind the column to the row (0 where the column is behind it)
+      float2 e[8];
+      float sum = half == 0 && lane >= 16 ? D.mid[t] : 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; j += 2) {
-        const float4 f = f4(D.pre + 32 * b + 16 * half + 2 * j), d = f4(D.d + 32 * b + 16 * half + 2 * j);
-        e[j] = __fmul2_rn(make_float2(d.x, d.y), make_float2(ex2(pre - f.x), ex2(pre - f.y)));
-        e[j + 1] = __fmul2_rn(make_float2(d.z, d.w), make_float2(ex2(pre - f.z), ex2(pre - f.w)));
+      for (int j = 6; j >= 0; j -= 2) {
+        const float4 d = f4(D.d + 32 * b + 16 * half + 2 * j);
+        float f[4];
+        const float dd[4] = {d.x, d.y, d.z, d.w};
+#pragma unroll
+        for (int k = 3; k >= 0; --k) {
+          f[k] = dd[k] * ex2(sum);
+          if (2 * j + k <= row) sum = fmaf(dd[k], A2, sum);
+        }
+        e[j] = make_float2(f[0], f[1]);
+        e[j + 1] = make_float2(f[2], f[3]);
       }
       tmem_ld_wait(v);
 #pragma unroll
@@ -587,7 +602,7 @@ __global__ void __launch_bounds__(NT, 1)
     for (int j = 0; j < kAhead; ++j) fetch(j, j);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      float d[NB], up[NB], s[NB];
+      float d[NB], up[NB], mid[NB], s[NB];
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         d[k] = __bfloat162float(raw[k][0]) + bias;
@@ -602,8 +617,10 @@ __global__ void __launch_bounds__(NT, 1)
       for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
-          const float u = __shfl_up_sync(~0u, up[k], o), v = __shfl_down_sync(~0u, s[k], o);
-          if (lane >= o) up[k] += u;
+          if (o == 16) mid[k] = up[k];
+          const float u = o < 16 ? __shfl_up_sync(~0u, up[k], o) : __shfl_sync(~0u, up[k], 15);
+          const float v = __shfl_down_sync(~0u, s[k], o);
+          if (o < 16 ? (lane & 15) >= o : lane >= 16) up[k] += u;
           if (lane + o < 32) s[k] += v;
         }
       }
@@ -616,6 +633,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (lane == 31) D.total[b0 + k] = up[k];
         D.d[32 * (b0 + k) + lane] = d[k];
         D.pre[32 * (b0 + k) + lane] = up[k];
+        if (kOut) D.mid[32 * (b0 + k) + lane] = mid[k];
       }
       x.arrive(TOTALS);
       if (!x.wait(TOTALS, i)) break;
