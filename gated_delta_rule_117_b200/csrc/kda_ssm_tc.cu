@@ -8,7 +8,7 @@
 //     G  = C B^T      128 x 128 x N      scores
 //     Yx = C S        128 x 64 x N       what the entering state gives
 //     dS = B^T wx     128 x 64 x 128     (wx = d 2^{L_127 - L} x, in three bf16 terms)
-//     Yi = W x        128 x 64 x 128     (W = G masked and decayed, A operand in TMEM)
+//     Yi = W x        128 x 64 x 128     (W = G masked and decayed, in two bf16 terms, A operand in TMEM)
 // Every exponent is a sum of l over exactly the tokens that it spans, all of one sign,
 // never a difference of two sums: decays as small as those of one token keep their
 // relative accuracy beside a step that wipes the state out (1e4 and more, where a
@@ -19,9 +19,11 @@
 //
 // Rounding.  The state lives in fp32 registers; what is added to it is split into
 // three bf16 terms (24 bits), so the state keeps fp32 accuracy: one bf16 would be off
-// by up to 2^-8 of every update for good, and two by 2^-16.  W and the copy of S that
-// outputs read are single bf16: what they cost an output (2.1e-3 of it in the mean
-// square, with its own rounding, against 1.7e-3 for that rounding alone) is not carried on.
+// by up to 2^-8 of every update for good, and two by 2^-16.  W is split into two (16 bits):
+// single, it cost an output up to 2.3e-3 of it in the mean square, where its own rounding to
+// bf16 is 1.66e-3 (2.09e-3 at 131,072 tokens of 16 heads, 1.67e-3 with the second term, which
+// takes 8 % of the time).  Only the copy of S that outputs read is single bf16: 1.84e-3 at worst
+// measured (decays of 1e-3 a token), not carried on from token to token.
 //
 // What bounds it: shared memory.  A chunk's products read 208 KB of it (with N = 64
 // columns an operand pair feeds the tensor core at 48 cycles a step for its 32), loads
@@ -39,7 +41,8 @@
 //                chunks ahead); warps 24-27 in a state pass
 //   warp 2       issues every MMA
 //   warps 4-11   scores: two threads own row t of G, half a block of columns each;
-//                they write W to TMEM
+//                they write W in G's place, up to the row's own block (the MMA leaves a row out
+//                where W has nothing: 64 columns of zeros a chunk and row need not be written)
 //   warps 12-15  tokens: thread t writes row t of wx (with warps 4-11, in a state pass)
 //   warps 16-23  state: two threads own row n of S, 32 columns (fp32 registers)
 //                each; they write the bf16 copy, the snapshots and the final state
@@ -124,7 +127,8 @@ static_assert(kBarOff + 8 * BARS <= kMisc, "barriers");
 // TMEM columns
 constexpr uint32_t kCols = 512;
 // (state pass: dS twice, at 0 and 192)
-constexpr uint32_t tG = 0, tW = 128, tDS = 192, tYi = 384, tYx = 448;  // dS: one block of 64 for each term of wx
+constexpr uint32_t tG = 0, tDS = 192, tYi = 384, tYx = 448;  // dS: one block of 64 for each term of wx
+// W takes the place of G: the 16 scores of a K step become 8 columns of first terms and 8 of second ones
 
 // A state pass has no C, S or y, so it has room for two wx and two dS: wx of a chunk is
 // written while the products of the one before run.  And as its chunks are short against
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(NT, 1)
       const uint64_t dX = sdesc_sw128(sbase + L::X + st * 16384, 16, 1024);
       if (!x.wait2(kOut ? F_BX : F_B, i)) break;
       if (kOut) {
-        // (the G before was read before its W was ready)
+        // (the W in G's place is read: YX_READY comes after the outputs of the chunk before)
         // Yx first: it waits longest for what it reads, and C is free for the next chunk once both
         // are done (G first: 2.44 us a chunk against 2.36)
         if (!x.wait(F_C, i) || !x.wait(YX_READY, i)) break;
@@ -495,7 +499,8 @@ __global__ void __launch_bounds__(NT, 1)
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) mma_bf16_ts(tb + tYi, tb + tW + 8 * k, sdesc_add(dX, k * 2048), idYx, k > 0);
+          for (int k = 0; k < 16; ++k)  // (rows before the step's block of tokens: no part of W)
+            mma_bf16_ts(tb + tYi, tb + tG + 8 * k, sdesc_add(dX, (k >> 1) * 2048), idYx, (1u << (k >> 2)) - 1, k > 0);
           mma_commit(&x.bar[Y_DONE + st]);
           mma_commit(&x.bar[BX_FREE + st]);
         }
@@ -510,44 +515,18 @@ __global__ void __launch_bounds__(NT, 1)
   } else if (kOut && warp >= 4 && warp < 12) {
     // ======================= scores =======================
     const int b = warp & 3, half = (warp - 4) >> 2;  // this warp's rows are block b, its columns a half of each block
-    const uint32_t tg = tl + tG + 16 * half, tw = tl + tW + 8 * half;
+    const uint32_t tg = tl + tG + 16 * half;
     const float A2 = a.A[h] * 1.4426950408889634f;
     const int row = lane - 16 * half;  // the diagonal block's columns of this half up to the row
-    {  // tokens behind this warp's block: zeros, once
-      const uint32_t z[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-#pragma unroll 1
-      for (int c = b + 1; c < 4; ++c) tmem_st8(tw + 16 * c, z);
-      tmem_st_wait();
-    }
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       if (!x.wait4(DEC, i)) break;
       const Decays &D = x.dec(i);
       const float pre = D.pre[t], rowf = ex2(pre);
       const float2 r2 = make_float2(rowf, rowf);
-      if (!x.wait(G_DONE, i)) break;
-      if (i >= 1 && !x.wait2(Y_DONE, i - 1)) break;  // W is read
-      tc_fence_after();
-      float v[16];
-      uint32_t w[8];
-      tmem_ld16(tg, v);
-#pragma unroll 1
-      for (int c = 0; c < b; ++c) {
-        const float *col = D.col[b - c - 1] + 32 * c + 16 * half;
-        tmem_ld_wait(v);
-#pragma unroll
-        for (int j = 0; j < 16; j += 4) {
-          const float4 f = f4(col + j);
-          const float2 lo = __fmul2_rn(make_float2(v[j], v[j + 1]), __fmul2_rn(r2, make_float2(f.x, f.y)));
-          const float2 hi = __fmul2_rn(make_float2(v[j + 2], v[j + 3]), __fmul2_rn(r2, make_float2(f.z, f.w)));
-          w[j / 2] = pack_bf16x2(lo.x, lo.y);
-          w[j / 2 + 1] = pack_bf16x2(hi.x, hi.y);
-        }
-        tmem_ld16(tg + 32 * (c + 1), v);
-        tmem_st8(tw + 16 * c, w);
-      }
-      // the diagonal block's factors, formed while its scores arrive: from the half's last column
-      // back, with the sum of l from behind the column to the row (0 where the column is behind it)
+      // the diagonal block's factors, formed before the scores arrive (131,072 tokens of 16 heads: 838 us
+      // formed between them, 824 so): from the half's last column back, with the sum of l from behind
+      // the column to the row (0 where the column is behind it)
       float2 e[8];
       float sum = half == 0 && lane >= 16 ? D.mid[t] : 0.f;
 #pragma unroll
@@ -563,15 +542,39 @@ __global__ void __launch_bounds__(NT, 1)
         e[j] = make_float2(f[0], f[1]);
         e[j + 1] = make_float2(f[2], f[3]);
       }
+      if (!x.wait(G_DONE, i)) break;
+      tc_fence_after();
+      float v[16];
+      uint32_t w[8], rest[8];
+      tmem_ld16(tg, v);
+#pragma unroll 1
+      for (int c = 0; c < b; ++c) {
+        const float *col = D.col[b - c - 1] + 32 * c + 16 * half;
+        tmem_ld_wait(v);
+#pragma unroll
+        for (int j = 0; j < 16; j += 4) {
+          const float4 f = f4(col + j);
+          float2 lo = __fmul2_rn(make_float2(v[j], v[j + 1]), __fmul2_rn(r2, make_float2(f.x, f.y)));
+          float2 hi = __fmul2_rn(make_float2(v[j + 2], v[j + 3]), __fmul2_rn(r2, make_float2(f.z, f.w)));
+          w[j / 2] = take_term(lo);
+          rest[j / 2] = pack_bf16x2(lo.x, lo.y);
+          w[j / 2 + 1] = take_term(hi);
+          rest[j / 2 + 1] = pack_bf16x2(hi.x, hi.y);
+        }
+        tmem_ld16(tg + 32 * (c + 1), v);
+        tmem_st16(tg + 32 * c, w, rest);
+      }
       tmem_ld_wait(v);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const float2 r = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), e[j]);
+        float2 r = __fmul2_rn(make_float2(v[2 * j], v[2 * j + 1]), e[j]);
         // columns behind the row: zeros, whatever the scores and factors are
         const int behind = 16 * half + 2 * j - lane;
-        w[j] = pack_bf16x2(r.x, r.y) & (behind < 0 ? ~0u : behind == 0 ? 0xffffu : 0u);
+        const uint32_t mask = behind < 0 ? ~0u : behind == 0 ? 0xffffu : 0u;
+        w[j] = take_term(r) & mask;
+        rest[j] = pack_bf16x2(r.x, r.y) & mask;
       }
-      tmem_st8(tw + 16 * b, w);
+      tmem_st16(tg + 32 * b, w, rest);
       tmem_st_wait();
       tc_fence_before();
       x.arrive(W_READY);

@@ -166,11 +166,14 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
 }
-// 8 consecutive 32-bit columns of the warp's 32 lanes <- one register per column and lane.
-__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint32_t (&r)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(r[0]), "r"(r[1]),
-               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(taddr)
-               : "memory");
+// 16 consecutive 32-bit columns of the warp's 32 lanes <- one register per column and lane: r[0..7], then q[0..7].
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[8], const uint32_t (&q)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(q[0]), "r"(q[1]), "r"(q[2]),
+      "r"(q[3]), "r"(q[4]), "r"(q[5]), "r"(q[6]), "r"(q[7]), "r"(taddr)
+      : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Per-warpgroup register budget (all four warps of a warpgroup execute it).
@@ -269,14 +272,16 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 // A from tensor memory: lane = row, each 32-bit column two consecutive K elements
-// (K-major), so a K = 16 step is 8 columns.
+// (K-major), so a K = 16 step is 8 columns.  `skip`: bit i set leaves lanes 32 i .. 32 i + 31
+// of the result as they are, whatever A holds there.
 __device__ __forceinline__ void mma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                            bool accumulate) {
+                                            uint32_t skip, bool accumulate) {
   asm volatile(
       "{\n\t.reg .pred p;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u)
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%5, %6, %7, %8}, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate ? 1u : 0u), "r"(skip & 1 ? ~0u : 0u), "r"(skip & 2 ? ~0u : 0u),
+      "r"(skip & 4 ? ~0u : 0u), "r"(skip & 8 ? ~0u : 0u)
       : "memory");
 }
 __device__ __forceinline__ void mma_commit_warp(uint64_t *bar) {
