@@ -122,11 +122,13 @@ __global__ void __launch_bounds__(kThreads) block_map_kernel(MapArgs a) {
 }  // namespace
 
 cudaError_t launch_block_map(const MapArgs &a, cudaStream_t st) {
+  // The attribute is the kernel's, not the call's: always the most that a call may need, so that
+  // calls of several host threads agree on it.
+  constexpr int kMaxSmem = 3 * sizeof(int) * (kMaxR + 1);
+  static_assert(kMaxSmem <= 200 * 1024, "prefix sums in shared memory");
   const size_t smem = 3 * sizeof(int) * ((size_t)a.R + 1);
-  static_assert(3 * sizeof(int) * (kMaxR + 1) <= 200 * 1024, "prefix sums in shared memory");
   if (smem > 48 * 1024) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(block_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = cudaFuncSetAttribute(block_map_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
     if (e != cudaSuccess) return e;
   }
   const int grid = max(1, (int)(((int64_t)a.rows + kRowsPerBlock - 1) / kRowsPerBlock));
