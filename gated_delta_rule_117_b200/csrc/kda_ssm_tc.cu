@@ -59,7 +59,9 @@
 //
 // Handovers are mbarriers, one completion a chunk; a barrier is a ring of two
 // where a waiter may fall a whole chunk behind.  Every wait is bounded: one that
-// gives up records KDA_ERR_TIMEOUT, and the CTA drains and returns.
+// gives up records KDA_ERR_TIMEOUT, and the CTA drains and returns: its loads have
+// landed and its MMAs are done before shared and tensor memory are given up, however
+// short the limit of the waits is (the drain has a limit of its own).
 #include <cuda_bf16.h>
 
 #include "kda_ssm_seg.cuh"
@@ -120,6 +122,7 @@ enum {
   F_B,        // [2] state pass: B landed
   B_FREE = F_B + 2,  // [2] state pass: B read
   DRAIN = B_FREE + 2,  // every MMA issued is done
+  NEVER,      // nothing arrives here: the wait of an injected stall (failure-detection tests)
   BARS
 };
 static_assert(kBarOff + 8 * BARS <= kMisc, "barriers");
@@ -153,7 +156,11 @@ struct TcArgs {
   int seg;
   float *ws, *decays;
   uint64_t wait_ns;
+  int stall;  // the MMA warp first waits on a barrier that nothing arrives on (failure-detection tests)
 };
+
+// Limit of the drain at the end of a CTA: far beyond what a load or an MMA in flight takes.
+constexpr uint64_t kDrainNs = 2000000000ull;
 
 // What a wait needs when it does not succeed at once (shared memory).
 struct Misc {
@@ -181,6 +188,16 @@ __device__ __noinline__ bool wait_slow(uint64_t *bar, uint32_t parity, Misc *m) 
     }
   }
   return __all_sync(~0u, ok);
+}
+
+// Waits for something that is in flight and ends by itself.
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, unsigned *status) {
+  const uint64_t t0 = global_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 1000000u))
+    if (global_ns() - t0 > kDrainNs) {
+      atomicExch(status, kDevTimeout);
+      break;
+    }
 }
 
 __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Misc *m) {
@@ -397,11 +414,10 @@ __global__ void __launch_bounds__(NT, 1)
     // ======================= producer =======================
     const uint32_t half = NK > 4 ? 32768u : 16384u;  // bytes of a B or C tile that are loaded
     int loads = 0, bloads = 0, cloads = 0;
-    bool ok = true;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1, row = row_of_seq + ch.first(i);
-      if (i >= 2 && !(ok = x.wait2(BX_FREE, i - 2))) break;
+      if (i >= 2 && !x.wait2(BX_FREE, i - 2)) break;
       const int f_b = kOut ? F_BX : F_B;
       if (elect_one()) {
         mbar_arrive_expect_tx(&x.bar[F_BX + st], 16384u + (kOut ? half : 0u));
@@ -409,7 +425,7 @@ __global__ void __launch_bounds__(NT, 1)
       }
       __syncwarp();
       loads = i + 1;
-      if (!kOut && i >= 2 && !(ok = x.wait2(B_FREE, i - 2))) break;
+      if (!kOut && i >= 2 && !x.wait2(B_FREE, i - 2)) break;
       if (elect_one()) {
         if (!kOut) mbar_arrive_expect_tx(&x.bar[f_b + st], half);
 #pragma unroll
@@ -419,7 +435,7 @@ __global__ void __launch_bounds__(NT, 1)
       __syncwarp();
       bloads = i + 1;
       if (kOut) {
-        if (i >= 1 && !(ok = x.wait(C_FREE, i - 1))) break;
+        if (i >= 1 && !x.wait(C_FREE, i - 1)) break;
         if (elect_one()) {
           mbar_arrive_expect_tx(&x.bar[F_C], half);
 #pragma unroll
@@ -437,20 +453,12 @@ __global__ void __launch_bounds__(NT, 1)
         __syncwarp();
       }
     }
-    if (!ok) {  // loads in flight must land before shared memory is given up
-      const uint64_t t0 = global_ns();
-      auto landed = [&](int b, int n) {  // the last two of n loads
-#pragma unroll 1
-        for (int k = max(0, n - 2); k < n; ++k)
-          while (!mbar_try_wait_sleep(&x.bar[b + (k & 1)], (k >> 1) & 1, 1000000u))
-            if (global_ns() - t0 > p.wait_ns) break;
-      };
-      landed(F_BX, loads);
-      if (!kOut) landed(F_B, bloads);
-      if (cloads > 0)
-        while (!mbar_try_wait_sleep(&x.bar[F_C], (cloads - 1) & 1, 1000000u))
-          if (global_ns() - t0 > p.wait_ns) break;
-    }
+    // the last loads must land before shared memory is given up (where the other roles gave up they
+    // may still be in flight, however few chunks there are)
+    for (int k = max(0, loads - 2); k < loads; ++k) drain(&x.bar[F_BX + (k & 1)], (k >> 1) & 1, a.q.status);
+    if (!kOut)
+      for (int k = max(0, bloads - 2); k < bloads; ++k) drain(&x.bar[F_B + (k & 1)], (k >> 1) & 1, a.q.status);
+    if (cloads > 0) drain(&x.bar[F_C], (cloads - 1) & 1, a.q.status);
   } else if (warp == 2) {
     // ======================= MMA issue =======================
     const uint32_t idG = idesc_bf16(128, 128, false, false, false);
@@ -460,6 +468,7 @@ __global__ void __launch_bounds__(NT, 1)
     const uint64_t dC = sdesc_sw128(sbase + kC, 16, 1024);
     // byte offset of K step k in a [128 x 128] tile, K along its rows
     auto koff = [](int k) { return (uint32_t)((k >> 2) * 16384 + (k & 3) * 32); };
+    if (p.stall) x.wait(NEVER, 0);  // (gives up, and every wait after it)
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int st = i & 1;
@@ -509,9 +518,7 @@ __global__ void __launch_bounds__(NT, 1)
     }
     if (elect_one()) mma_commit(&x.bar[DRAIN]);
     __syncwarp();
-    const uint64_t t0 = global_ns();
-    while (!mbar_try_wait_sleep(&x.bar[DRAIN], 0, 1000000u))
-      if (global_ns() - t0 > p.wait_ns) break;
+    drain(&x.bar[DRAIN], 0, a.q.status);
   } else if (kOut && warp >= 4 && warp < 12) {
     // ======================= scores =======================
     const int b = warp & 3, half = (warp - 4) >> 2;  // this warp's rows are block b, its columns a half of each block
@@ -907,6 +914,7 @@ cudaError_t launch_ssm_tc(const SsmArgs &a, int seg, cudaStream_t st) {
   p.ws = seg ? seg_states(a) : nullptr;
   p.decays = seg ? seg_decays(a, items) : nullptr;
   p.wait_ns = debug_wait_ns();
+  p.stall = debug_stall();
   const unsigned grid = (unsigned)(items * a.H * ((a.P + PC - 1) / PC));
   switch (a.N) {
     case 16: return launch_nk<1>(mx, mb, mc, my, p, grid, st);

@@ -514,7 +514,7 @@ kda_status_t kda_get_device_status(kda_stream_t stream);
 
 /*
  * Failure-detection testing aids (host-side fault injection; never needed in
- * production).  The tensor-core prefill kernel's cross-role waits are bounded:
+ * production).  The cross-role waits of the tensor-core kernels (prefill, scan) are bounded:
  * a wait that does not complete within the limit aborts the CTA (no further
  * tensor-core work, every issued copy and MMA drained before its tensor memory
  * is released), records KDA_ERR_TIMEOUT in the device status word and returns,
@@ -522,7 +522,7 @@ kda_status_t kda_get_device_status(kda_stream_t stream);
  *
  * kda_debug_set_wait_limit: wall-time limit of those waits for calls enqueued
  *   afterwards, in nanoseconds (0 restores the default of 2 s).  Process-wide.
- * kda_debug_inject_stall: when on, prefill calls on the tensor-core path
+ * kda_debug_inject_stall: when on, prefill calls and scans on the tensor-core path
  *   enqueued afterwards first wait on a barrier nothing ever arrives on, so
  *   the wait runs out after the limit above and the call aborts as described.
  *   Process-wide; turn it off again to resume normal operation.
