@@ -76,6 +76,12 @@ struct Seq {
 
 __device__ __forceinline__ void record_bounds(unsigned *status) { atomicCAS(status, kDevOk, kDevBounds); }
 
+// Offsets that lead outside the rows, whether or not any block comes to the sequence (one thread
+// of a call does this).
+__device__ __forceinline__ void tell_offsets(const Requests &q) {
+  if (q.cu && (q.cu[0] < 0 || q.cu[q.R] > q.rows)) record_bounds(q.status);
+}
+
 // Rows and slot of sequence r.  `tell`: record values that lead outside.
 __device__ __forceinline__ Seq seq_of(const Requests &q, int r, bool tell) {
   Seq s;

@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(kThreads, blocks_of(NORM)) short_conv_kernel(C
   T *pool = a.state ? (T *)a.state + c0 : nullptr;
   const int64_t xs = a.x_stride;
 
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) tell_offsets(q);
   int total = q.rows, r;
   if (q.cu) {
     total = min(q.cu[q.R], q.rows);

@@ -62,6 +62,7 @@ __device__ __forceinline__ int sequence_of_rank(const Requests &q, int item, int
 // The block's work item; false: none.  Every thread of the block must call it;
 // `scratch` as above.
 __device__ __forceinline__ bool item_of(const Requests &q, int item, int seg, int align, bool tell, int *scratch, Item &it) {
+  if (tell && item == 0) tell_offsets(q);
   if (seg == 0) {
     it.r = q.cu && q.R > 1 && q.R <= kMaxRanked ? sequence_of_rank(q, item, scratch) : item;
   } else {
