@@ -61,8 +61,13 @@ cudaError_t launch_block_map(const MapArgs &a, cudaStream_t s);
 cudaError_t launch_short_conv(const ConvArgs &a, cudaStream_t s);
 cudaError_t launch_short_conv_step(const ConvArgs &a, cudaStream_t s);
 cudaError_t launch_ssm_step(const SsmArgs &a, cudaStream_t s);
-cudaError_t launch_ssm_scan(const SsmArgs &a, cudaStream_t s);
-size_t ssm_scan_workspace(int R, int rows, int H, int G, int N, int P, int bf16);
+// How a scan cuts its sequences: seg[tensor cores][packed] tokens (0: whole sequences).
+struct ScanPlan {
+  int seg[2][2];
+  size_t workspace;
+};
+ScanPlan plan_ssm_scan(int R, int rows, int H, int N, int P, int bf16);
+cudaError_t launch_ssm_scan(const SsmArgs &a, const ScanPlan &plan, cudaStream_t s);
 
 // ---- device side ---------------------------------------------------------------
 

@@ -196,7 +196,9 @@ kda_status_t check_ssm_sizes(int H, int G, int N, int P, kda_dtype_t dtype) {
   return KDA_OK;
 }
 
-// One block for each (segment, head, slice of P), and segments of at least 128 tokens.
+// The blocks of a launch, one for each (segment, head, slice of P), with segments of 128 tokens:
+// the tensor-core kernel's are longer, and shorter ones of the CUDA-core kernel are taken only
+// where their blocks fit as well.
 bool scan_grid_fits(int R, int rows, int H) {
   return ((int64_t)rows / 128 + 2 * (int64_t)R) <= INT32_MAX / (2 * (int64_t)(H > 0 ? H : 1));
 }
@@ -242,7 +244,7 @@ size_t kda_ssm_scan_workspace_size(int R, int rows, int H, int G, int N, int P, 
   if (R < 0 || rows < 0 || check_ssm_sizes(H, G, N, P, dtype) != KDA_OK) return (size_t)-1;
   if (R == 0 || rows == 0 || H == 0) return 0;
   if (rows > kMaxRows || !scan_grid_fits(R, rows, H)) return (size_t)-1;
-  return kda::ssm_scan_workspace(R, rows, H, G, N, P, dtype == KDA_DTYPE_BF16);
+  return kda::plan_ssm_scan(R, rows, H, N, P, dtype == KDA_DTYPE_BF16).workspace;
 }
 
 kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
@@ -261,7 +263,8 @@ kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64
   if (!scan_grid_fits(R, rows, H)) return KDA_ERR_SHAPE;
   const bool snap = page_size > 0 && table_stride > 0 && n_pages > 0;
   if (snap && (!block_table || !pages)) return KDA_ERR_INVALID_ARG;
-  const size_t need = kda::ssm_scan_workspace(R, rows, H, G, N, P, dtype == KDA_DTYPE_BF16);
+  const kda::ScanPlan plan = kda::plan_ssm_scan(R, rows, H, N, P, dtype == KDA_DTYPE_BF16);
+  const size_t need = plan.workspace;
   if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   kda::SsmArgs a;
   a.q = kda::Requests{cu, ctx, slots, R, rows, rows / R, n_slots, nullptr};
@@ -282,7 +285,7 @@ kda_status_t kda_ssm_scan(const void *x, int64_t x_stride, const void *dt, int64
   if (st != KDA_OK) return st;
   a.q.status = kda::device_status_ptr();
   if (!a.q.status) return KDA_ERR_CUDA;
-  return kda::launch_ssm_scan(a, (cudaStream_t)stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
+  return kda::launch_ssm_scan(a, plan, (cudaStream_t)stream) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
 kda_status_t kda_ssm_step(const void *x, int64_t x_stride, const void *dt, int64_t dt_stride, const float *A,
