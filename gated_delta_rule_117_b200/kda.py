@@ -628,11 +628,11 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
         _too_large()
     given = cu is not None or token_slots is not None or pages_used is not None
     if cu is None:
-        cu = _fresh(stream, lens.new_empty, R + 1)
+        cu = _fresh(stream, d, lens.new_empty, R + 1)
     if token_slots is None:
-        token_slots = _fresh(stream, lens.new_empty, rows, dtype=torch.int64)
+        token_slots = _fresh(stream, d, lens.new_empty, rows, dtype=torch.int64)
     if pages_used is None:
-        pages_used = _fresh(stream, lens.new_empty, 1)
+        pages_used = _fresh(stream, d, lens.new_empty, 1)
     if given:
         _shaped("cu", cu, (R + 1,))
         _shaped("token_slots", token_slots, (rows,))
@@ -647,23 +647,24 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
     return cu, token_slots, pages_used
 
 
-def _on_stream(stream):
-    """A context whose allocations belong to the stream that will use them (`stream`: a torch stream or a handle)."""
-    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(stream))
+def _on_stream(stream, d):
+    """A context whose allocations belong to the stream that will use them (`stream`: a torch stream or, of device d,
+    a handle)."""
+    return _torch.cuda.stream(stream if hasattr(stream, "cuda_stream") else _torch.cuda.ExternalStream(stream, device=d))
 
 
-def _fresh(stream, make, *args, **kw):
-    """make(*args, **kw): a tensor that belongs to the call's stream (None: the current one)."""
+def _fresh(stream, d, make, *args, **kw):
+    """make(*args, **kw): a tensor on device d that belongs to the call's stream (None: the current one)."""
     if stream is None:
         return make(*args, **kw)
-    with _on_stream(stream):
+    with _on_stream(stream, d):
         return make(*args, **kw)
 
 
 def _output(x, y, lead, width, stream):
     """(y, its row stride) for a token-major output like x."""
     if y is None:
-        return _fresh(stream, _torch.empty_like, x, memory_format=_torch.contiguous_format), width
+        return _fresh(stream, x.get_device(), _torch.empty_like, x, memory_format=_torch.contiguous_format), width
     _typed(x.dtype, "y", y)
     _shaped("y", y, x.shape)
     _on(x, y)
@@ -708,7 +709,7 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
             raise ValueError("head_major needs a head_dim that divides C")
         shape, ys = (R, C // head_dim, rows // max(R, 1), head_dim), C
         if y is None:
-            y = _fresh(stream, torch.empty, shape, dtype=x.dtype, device=x.device)
+            y = _fresh(stream, d, torch.empty, shape, dtype=x.dtype, device=x.device)
         else:
             _typed(x.dtype, "y", y)
             _shaped("y", y, shape)
@@ -809,7 +810,7 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
     wbytes = 0
     if ws > 0 and workspace is None:
         # (it is given back when this returns, maybe before the stream is done with it)
-        workspace = _fresh(stream, torch.empty, ws, dtype=torch.uint8, device=x.device)
+        workspace = _fresh(stream, d, torch.empty, ws, dtype=torch.uint8, device=x.device)
     if workspace is not None:
         _dense("workspace", workspace)
         _on(x, workspace)
