@@ -207,7 +207,7 @@ int simt_segment(int R, int rows, int H, int N, int P, bool packed) {
   return seg;
 }
 
-// The tensor-core kernel, in tokens of an output pass: one block an SM; a chunk takes 2.3 us,
+// The tensor-core kernel, in tokens of an output pass: one block an SM; a chunk takes 2.45 us,
 // 1.2 us in the state pass; a block's beginning and end 6 us, the two launches about 10 us.
 // 131,072 tokens of 16 heads of 128 in 9 segments: state pass 279 us, join 7 us, outputs 529 us.
 int tc_segment(int R, int rows, int H, int P, bool packed) {
@@ -217,12 +217,12 @@ int tc_segment(int R, int rows, int H, int P, bool packed) {
   // blocks of unequal length fill the machine as they come: the waves' total, or the longest block
   double best = packed ? fmax(most, (mean + begin) * R * blocks) : ceil(R * blocks) * (mean + begin);
   int seg = 0;
-  if (1.53 * rows * blocks >= best) return 0;
+  if (1.49 * rows * blocks >= best) return 0;
   for (int k = 2; k <= 64; k = next_count(k)) {
     const int len = (int)((mean / k + kAlign - 1) / kAlign) * kAlign;
     if (len < 4 * kAlign) break;
     const double items = packed ? rows / (double)len + 0.5 * R : (double)R * ceil(mean / len);
-    const double cost = ceil(items * blocks) * (len + begin) * 1.53 + 4 * kAlign;
+    const double cost = ceil(items * blocks) * (len + begin) * 1.49 + 4 * kAlign;
     if (cost < best) {
       best = cost;
       seg = len;
@@ -288,7 +288,7 @@ static bool tokens_are_few(const SsmArgs &a) {
   };
   const double waves = fmax(1, states * ((a.P + 63) / 64) / 148);
   const double tc = waves * (mean <= kShort ? 3.8 + 0.015 * a.N + mean * (0.12 + 0.001 * a.N)
-                                            : 6 + 0.02 * a.N + 2.3 * floor((mean - 1) / kAlign));
+                                            : 6 + 0.02 * a.N + 2.45 * floor((mean - 1) / kAlign));
   return a.q.cu ? simt(fmin(a.q.rows, 2 * mean)) * simt(a.q.rows) < tc * tc : simt(mean) < tc;
 }
 
