@@ -624,7 +624,7 @@ def block_map(lens, ctx, free_pages, block_table, page_size, rows, *, cu=None, t
         _on(lens, ctx, free_pages, block_table)
         _shaped("ctx", ctx, (R,))
         raise ValueError("lens and ctx must be [R], free_pages [n], block_table [R, blocks]")
-    if max(R, rows, n_free, shape[1], page_size) > _INT_MAX:
+    if (R | rows | n_free | shape[1]) > _INT_MAX or page_size > _INT_MAX:
         _too_large()
     given = cu is not None or token_slots is not None or pages_used is not None
     if cu is None:
@@ -700,7 +700,7 @@ def short_conv(x, w, bias=None, *, state=None, slots=None, ctx=None, cu=None, si
     C, d = x.shape[lead], x.get_device()
     K, n_slots = _conv_weights(x, w, bias, state, C, d)
     R, rows = _requests(x, lead, slots, ctx, cu, d)
-    if max(R, rows, C, n_slots, head_dim) > _INT_MAX:
+    if (R | rows | C | n_slots) > _INT_MAX or head_dim > _INT_MAX:
         _too_large()
     if not head_major:
         y, ys = _output(x, y, lead, C, stream)
@@ -736,7 +736,7 @@ def short_conv_step(x, w, state, bias=None, *, slots=None, silu=True, head_dim=0
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
-    if max(R, C, n_slots, head_dim) > _INT_MAX:
+    if (R | C | n_slots) > _INT_MAX or head_dim > _INT_MAX:
         _too_large()
     y, ys = _output(x, y, 1, C, stream)
     flags = (KDA_CONV_SILU if silu else 0) | (KDA_CONV_L2NORM if l2norm else 0)
@@ -800,7 +800,7 @@ def ssm_scan(x, dt, A, B, C, D=None, dt_bias=None, *, softplus=True, state=None,
         _shaped("pages", pages, (n_pages, H, N, P))
     else:
         block_table = pages = None
-    if max(R, rows, n_slots, n_pages, width, page_size, H) > _INT_MAX:
+    if (R | rows | n_slots | n_pages | width | H) > _INT_MAX or page_size > _INT_MAX:
         _too_large()
     y, ys = _output(x, y, lead, H * P, stream)
     lib = load_library()
@@ -835,7 +835,7 @@ def ssm_step(x, dt, A, B, C, state, D=None, dt_bias=None, *, softplus=True, slot
     if not _good_slots(slots, R, d, torch.int32):
         _on(x, slots)
         _bad_requests(slots, None, None, R)
-    if max(R, n_slots, H) > _INT_MAX:
+    if (R | n_slots | H) > _INT_MAX:
         _too_large()
     y, ys = _output(x, y, 1, H * P, stream)
     _launch(load_library().kda_ssm_step, "kda_ssm_step", d, stream,
