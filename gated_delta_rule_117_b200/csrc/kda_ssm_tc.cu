@@ -22,18 +22,23 @@
 // by up to 2^-8 of every update for good, and two by 2^-16.  W is split into two (16 bits):
 // single, it cost an output up to 2.3e-3 of it in the mean square, where its own rounding to
 // bf16 is 1.66e-3 (2.09e-3 at 131,072 tokens of 16 heads, 1.67e-3 with the second term, which
-// takes 8 % of the time).  Only the copy of S that outputs read is single bf16: 1.84e-3 at worst
-// measured (decays of 1e-3 a token), not carried on from token to token.
+// takes 8 % of the time).  Only the copy of S that outputs read is single bf16, and what it costs is
+// not carried on from token to token.  By how much of an output the entering state makes up: 1.66e-3
+// to 1.67e-3 at steps d A of -0.1 and beyond, 1.81e-3 at -1e-3 (2.24e-3 without the skip term),
+// 2.33e-3 at worst (smaller steps, no skip term; 1.66e-3 with it).  A second term of it was built: y then
+// takes x's place in shared memory, 1.66e-3 throughout, and 870 us for those 131,072 tokens against 835.
 //
-// What bounds it: shared memory.  A chunk's products read 208 KB of it (with N = 64
-// columns an operand pair feeds the tensor core at 48 cycles a step for its 32), loads
-// and stores by TMA move 96 KB and the roles 128 KB: 3,400 cycles at 128 bytes a cycle.
-// Measured, 148 CTAs, N = 128: 4,100 to 4,300 cycles, 2.3 us a chunk (against 0.74 us
-// for its 32 KB of x and y at the copy rate), tensor pipe 47 % and issue slots 56 %
-// busy.  What was tried and lost: rows of y stored from registers instead of a staged
-// tile (2.99 us), the scores' diagonal factors before G or the outputs' tensor memory
-// read at once (2.35 and 2.42 against 2.33), the score warps sharing wx in output runs
-// (3.03).  Two terms instead of three are 7 % faster and lose the state's last 8 bits.
+// What bounds it: the score warps' path between G and Yi, and shared memory.  A chunk's
+// products read 224 KB (with N = 64 columns an operand pair feeds the tensor core at 48
+// cycles a step for its 32), loads and stores by TMA move 96 KB and the roles 128 KB: 3,500
+// cycles at 128 bytes a cycle.  Measured, 148 CTAs, N = 128: 4,600 cycles, 2.45 us a chunk
+// (against 0.74 us for its 32 KB of x and y at the copy rate), tensor pipe 44 % and issue
+// slots 54 % busy.  What was tried and lost: rows of y stored from registers instead of a
+// staged tile (2.99 us against 2.33), the outputs' tensor memory read at once (2.42 against
+// 2.33), the score warps sharing wx in output runs (3.03), Yx in two places of tensor memory so
+// that it need not wait for the outputs (the same), first terms of W cut instead of rounded
+// (857 us against 846).  Two terms of wx instead of three are 7 % faster and lose the state's
+// last 8 bits.
 //
 // Work split: one CTA a (segment, head, 64 columns of P), 32 warps of 64 registers:
 //   warp 0       producer: TMA loads of B, x (two stages) and C

@@ -376,7 +376,8 @@ size_t kda_noalloc_scratch_bytes(void);
  * or more, cu[R] > rows, a block of n_pages or more) are not followed: that
  * sequence or row is skipped and KDA_ERR_DEVICE recorded
  * (kda_get_device_status).  cu, ctx, slots: 4-byte aligned.  Outputs must not
- * overlap each other or any input.
+ * overlap each other or any input (from the first to the last element, whatever the row
+ * strides leave out between).
  */
 
 /*
@@ -465,7 +466,9 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
  *   below 2^30 (KDA_ERR_SHAPE beyond)
  * d_t A[h] <= 0 is relied on (d_t >= 0, which softplus gives).  State,
  * decays and sums are fp32; on the tensor-core path (bf16 with 16-byte aligned
- * rows) the products take bf16 operands, as noted at the kernel, and an input
+ * rows) the products take bf16 operands: the state's updates in three terms, the
+ * decayed scores in two, and the state that outputs read in one (2^-8 of its part of an
+ * output; the state itself does not lose it), and an input
  * that is not finite leaves its sequence's outputs undefined from up to 127
  * tokens before it (from the last multiple of 128 of the position) on.
  *
