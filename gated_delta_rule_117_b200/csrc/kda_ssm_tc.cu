@@ -548,11 +548,11 @@ __global__ void __launch_bounds__(NT, 1)
         const float dd[4] = {d.x, d.y, d.z, d.w};
 #pragma unroll
         for (int k = 3; k >= 0; --k) {
-          f[k] = dd[k] * ex2(sum);
+          f[k] = ex2(sum);
           if (2 * j + k <= row) sum = fmaf(dd[k], A2, sum);
         }
-        e[j] = make_float2(f[0], f[1]);
-        e[j + 1] = make_float2(f[2], f[3]);
+        e[j] = __fmul2_rn(make_float2(d.x, d.y), make_float2(f[0], f[1]));
+        e[j + 1] = __fmul2_rn(make_float2(d.z, d.w), make_float2(f[2], f[3]));
       }
       if (!x.wait(G_DONE, i)) break;
       tc_fence_after();
