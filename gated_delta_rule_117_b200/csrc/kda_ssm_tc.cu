@@ -25,7 +25,7 @@
 // takes 8 % of the time).  Only the copy of S that outputs read is single bf16, and what it costs is
 // not carried on from token to token.  By how much of an output the entering state makes up: 1.66e-3
 // to 1.67e-3 at steps d A of -0.1 and beyond, 1.81e-3 at -1e-3 (2.24e-3 without the skip term),
-// 2.33e-3 at worst (smaller steps, no skip term; 1.66e-3 with it).  A second term of it was built: y then
+// 2.33e-3 at worst (smaller steps, no skip term; 1.68e-3 with it).  A second term of it was built: y then
 // takes x's place in shared memory, 1.66e-3 throughout, and 870 us for those 131,072 tokens against 835.
 //
 // What bounds it: the score warps' path between G and Yi, and shared memory.  A chunk's
@@ -59,8 +59,9 @@
 // stages.
 // Columns of S are independent, so P = 128 is two CTAs (which form G twice: it
 // is a third of the tensor work and saves any exchange).  Rows behind a chunk's
-// last token are zeroed in the operands that sum over tokens, and not stored;
-// values that are not finite spoil their chunk's outputs, earlier tokens included.
+// last token are zeroed in the operands that sum over tokens, and not stored.  An x that is not
+// finite spoils the outputs of the earlier tokens of its block of 32 (0 times it); other
+// inputs that are not finite meet no earlier token.
 //
 // Handovers are mbarriers, one completion a chunk; a barrier is a ring of two
 // where a waiter may fall a whole chunk behind.  Every wait is bounded: one that

@@ -469,8 +469,8 @@ kda_status_t kda_short_conv_step(const void *x, int64_t x_stride, const void *w,
  * rows) the products take bf16 operands: the state's updates in three terms, the
  * decayed scores in two, and the state that outputs read in one (2^-8 of its part of an
  * output; the state itself does not lose it), and an input
- * that is not finite leaves its sequence's outputs undefined from up to 127
- * tokens before it (from the last multiple of 128 of the position) on.
+ * that is not finite leaves its sequence's outputs undefined from up to 31
+ * tokens before it on.
  *
  * State snapshots (section 5.4.1): with page_size > 0 (a multiple of 128) the
  * state after every position that is a multiple of page_size (counted with
